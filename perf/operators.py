@@ -487,9 +487,10 @@ def _fork(s):
     first = (s["lo"].long() // BLOCK)[:, None, None].expand(B, Hkv, 1)
     at = torch.cat([first, (first + 1).clamp_max(NB - 1)], -1)
     src, dst = was.view(B, Hkv, NB).gather(-1, at).view(-1), new.view(B, Hkv, NB).gather(-1, at).view(-1)
+    quiet = (~free).long().argmax()               # a page in use before: no fresh page, so nobody's destination
     src = torch.where(src >= 0, src, dst)
-    dst = torch.where(dst >= 0, dst, 0)
-    src = torch.where(src >= 0, src, 0)
+    dst = torch.where(dst >= 0, dst, quiet)       # nothing to copy: that page onto itself
+    src = torch.where(src >= 0, src, quiet)
     bb = _block_bytes(c["d"], c["group"])
     for name in ("k", "v"):
         data = s[name].view(pool, bb)
