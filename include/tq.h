@@ -292,6 +292,160 @@ TQ_API tq_status tq_attend_decode_static(const tq_handle* h, const void* q, tq_d
                                          const int32_t* seq_lens, int64_t T, float scale, float* out,
                                          void* stream);
 
+/* ---- 4-bit caches ------------------------------------------------------- */
+
+/* A cache of plain 4-bit codes with group scales, beside the TurboQuant
+ * caches: no rotation and no codebook, 4 + 32 / group bits per value (4.5 at
+ * group 64).  Each vector of d values is cut into groups of `group`
+ * consecutive values (32, 64 or 128, at most d).  A group stores an fp16 zero
+ * and an fp16 scale, a value stands for zero + scale * code:
+ *   x taken within +-65504;  zero = fp16(min x)
+ *   scale = fp16((max x - zero) * fp32(1/15));  r = 1 / scale (0 if scale <= 0)
+ *   code = min(15, max(0, rint((x - zero) * r)))     (half to even)
+ * each step one correctly rounded fp32 operation.  A group with a NaN stores
+ * NaN for both.  K and V have the same format.  The cache is a tq_cache
+ * (contiguous or paged, 64 tokens per block) whose blocks are
+ * tq_int4_block_bytes(d, group) long: codes 64 x d/2 B | (scale, zero) fp16
+ * pairs 64 x d/group x 4 B.  Byte j of token tau's codes (values 2j in the low,
+ * 2j + 1 in the high nibble) is stored at j ^ 16 s, s = (tau & 2 if d >= 128,
+ * else 0) + (4 (tau & 1) if d = 256, else 0). */
+
+/* Bytes of one 64-token block; 0 for an unsupported d or group. */
+TQ_API size_t tq_int4_block_bytes(int head_dim, int group);
+
+/* Bytes of a contiguous cache; 0 as tq_cache_bytes, or for an unsupported group. */
+TQ_API size_t tq_int4_cache_bytes(int head_dim, int group, int64_t B, int64_t Hkv, int64_t Tcap);
+
+/* Encode T new vectors per (batch, kv head); x, dtype and strides as
+ * tq_encode_k.  Token i of sequence b goes to position pos[b] + i (pos: device
+ * int32[B]), or t0 + i when pos is NULL.  Positions from pos outside
+ * [0, Tcap), and positions on a bad block-table entry, are skipped and
+ * reported by tq_device_status.  Other tokens are not touched.
+ * Errors: INVALID_ARG (as tq_encode_k; a bad group), UNSUPPORTED (2^31 words
+ * of 8 values or more), CUDA. */
+TQ_API tq_status tq_encode_int4(const tq_handle* h, int group, const void* x, tq_dtype dtype, int64_t B, int64_t Hkv,
+                                int64_t T, int64_t sb, int64_t sh, int64_t st, const tq_cache* c, const int32_t* pos,
+                                int64_t t0, void* stream);
+
+/* Read T tokens per (batch, kv head) back as values of `dtype` (fp32 value
+ * zero + scale * code rounded once); positions as tq_encode_int4, x is the
+ * output with its strides.  Vectors of skipped positions are left as they
+ * were.  Errors: as tq_encode_int4. */
+TQ_API tq_status tq_expand_int4(const tq_handle* h, int group, void* x, tq_dtype dtype, int64_t B, int64_t Hkv,
+                                int64_t T, int64_t sb, int64_t sh, int64_t st, const tq_cache* c, const int32_t* pos,
+                                int64_t t0, void* stream);
+
+/* Workspace bytes of tq_attend_int4 and tq_append_attend_int4 on this handle's
+ * device; it does not depend on the context length.  0 on bad arguments. */
+TQ_API size_t tq_attend_int4_workspace_bytes(const tq_handle* h, int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv);
+
+/* Attention of Lq >= 1 new queries per sequence over 4-bit caches (Lq = 1: a
+ * decode step; small Lq: speculative tokens; large Lq: a prefill chunk).
+ * q and out are [B][Lq][Hq][d] contiguous, both of `qdtype`.  Sequence b has
+ * n = seq_lens[b] tokens (device int32[B]; clamped to [0, Tcap]), or n = T when
+ * seq_lens is NULL, its Lq newest among them: query i attends over tokens
+ * [0, n - Lq + 1 + i), and a query that sees none gives zeros.  Query head h
+ * uses kv head h / (Hq/Hkv); scores are scale <q, k>, softmax and sums in fp32.
+ * What lies in the caches behind a query's last visible token has no effect on
+ * it, whatever it is.  Sequences may have any mixture of lengths: the work is
+ * shared out over the SMs on the device.  fp32 queries are taken to 22 bits
+ * relative to their row's largest element, 16-bit queries exactly.
+ * Supported: any Hq/Hkv, B < 2^31, Lq * Hq / Hkv < 2^31, Hkv * row groups <
+ * 2^31 (row groups: query rows per kv head / 4, rounded up); contiguous or
+ * paged caches.  ws: 256-byte aligned, at least
+ * tq_attend_int4_workspace_bytes(h, B, Lq, Hq, Hkv) bytes; two calls that may
+ * overlap on the GPU need two workspaces.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA. */
+TQ_API tq_status tq_attend_int4(const tq_handle* h, int group, const void* q, tq_dtype qdtype, int64_t B, int64_t Lq,
+                                int64_t Hq, const tq_cache* kc, const tq_cache* vc, const int32_t* seq_lens, int64_t T,
+                                float scale, void* out, void* ws, size_t ws_bytes, void* stream);
+
+/* One serving step: encode Lq new K and V vectors per (batch, kv head) at
+ * positions pos[b] + i (t0 + i when pos is NULL) of kc and vc, then attend
+ * with their Lq queries over the pos[b] + Lq tokens.  Results are those of
+ * tq_encode_int4 on both caches and tq_attend_int4 with seq_lens = pos + Lq.
+ * k_new and v_new share kv_dtype and strides.  The encodes are one launch, and
+ * the attention's set-up overlaps it.  kc and vc must not overlap.
+ * Errors: those of tq_encode_int4 and tq_attend_int4, before any launch. */
+TQ_API tq_status tq_append_attend_int4(const tq_handle* h, int group, const void* k_new, const void* v_new,
+                                       tq_dtype kv_dtype, int64_t Lq, int64_t sb, int64_t sh, int64_t st,
+                                       const tq_cache* kc, const tq_cache* vc, const int32_t* pos, int64_t t0,
+                                       const void* q, tq_dtype q_dtype, int64_t Hq, float scale, void* out, void* ws,
+                                       size_t ws_bytes, void* stream);
+
+/* ---- pages of paged caches ----------------------------------------------- */
+
+/* The pages that hold paged caches of any format, managed on the device so
+ * that a captured serving step needs no host bookkeeping.  block_table (device
+ * int32 [B*Hkv][NB], rows as tq_cache's, -1: no page) and refs (device
+ * int32[pool_blocks]) are the state: refs[p] is the number of table entries
+ * that name page p, and a page with 0 is free.  An empty state is a table of
+ * -1 and zero refs.  Page p is block p of each of the n_buffers pools
+ * `buffers` (device pointers, 16-byte aligned, in a host array) with
+ * block_bytes[i] bytes per page (multiples of 16): the K and the V pool of one
+ * layer or of several that share the table.  The same block_table goes into
+ * the tq_cache of each.  A cache whose pages are shared (refs > 1) must not be
+ * written there: tq_pages_alloc gives the writer its own copy first.
+ * Entries outside [-1, pool_blocks) are left alone and reported by
+ * tq_device_status, as are indices out of range.  Calls enqueue kernels, do
+ * not synchronise, and their outcome does not depend on thread order.  One
+ * call at a time may work on a state. */
+#define TQ_MAX_PAGE_BUFFERS 128
+typedef struct {
+    int32_t* block_table;
+    int32_t* refs;
+    int64_t B, Hkv, NB;
+    int64_t pool_blocks;
+    int32_t n_buffers;            /* 0 .. TQ_MAX_PAGE_BUFFERS */
+    void* const* buffers;         /* host array */
+    const int64_t* block_bytes;   /* host array */
+} tq_pages;
+
+/* Workspace bytes of tq_pages_alloc and tq_pages_compact; 0 on bad arguments. */
+TQ_API size_t tq_pages_workspace_bytes(const tq_pages* p);
+
+/* Make tokens [lo[b], hi[b]) of every sequence writable (device int32[B];
+ * lo = hi: nothing asked): a block of them without a page gets a fresh one,
+ * and a block whose page has refs > 1 gets a fresh copy of it (copy on write;
+ * the page loses one reference).  Fresh pages are the free ones in ascending
+ * order, given to the asking blocks in (row, block) order; contents of fresh
+ * pages that are no copies are undefined.  When the pool runs out the rest of
+ * the blocks stay as they are.  info (device int32[2], may be NULL): pages
+ * free afterwards, blocks left without.  Errors: INVALID_ARG, UNSUPPORTED
+ * (2^31 table entries or more), WORKSPACE, CUDA. */
+TQ_API tq_status tq_pages_alloc(const tq_handle* h, const tq_pages* p, const int32_t* lo, const int32_t* hi,
+                                int32_t* info, void* ws, size_t ws_bytes, void* stream);
+
+/* Every sequence b takes the pages of sequence parent[b] as they were before
+ * the call (device int32[B]; b itself: unchanged, -1: none): entries are
+ * shared, not copied, and refs follow on both sides.  Any mapping is allowed,
+ * exchanges and repeated parents included; a parent outside [-1, B) leaves its
+ * sequence unchanged and is reported.  Errors: INVALID_ARG, UNSUPPORTED
+ * (B > 7168, Hkv > 65535), CUDA. */
+TQ_API tq_status tq_pages_fork(const tq_handle* h, const tq_pages* p, const int32_t* parent, void* stream);
+
+/* Release what sequence b holds behind its first keep[b] tokens (device
+ * int32[B]; <= 0: everything): blocks from ceil(keep[b] / 64) on lose their
+ * page (entry -1, refs - 1).  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+TQ_API tq_status tq_pages_free(const tq_handle* h, const tq_pages* p, const int32_t* keep, void* stream);
+
+/* Move the live pages (refs > 0) into the lowest places of the pools: with L
+ * of them, the k-th lowest free page below L takes the contents and references
+ * of the k-th highest live page, and the table follows.  Pages from L on are
+ * free afterwards (their contents are left).  info (device int32[2], may be
+ * NULL): free pages, pages moved.  Errors: as tq_pages_alloc. */
+TQ_API tq_status tq_pages_compact(const tq_handle* h, const tq_pages* p, int32_t* info, void* ws, size_t ws_bytes,
+                                  void* stream);
+
+/* Copy pages src[i] of `from`'s buffers to pages dst[i] of `to`'s (device
+ * int32[n]), buffer by buffer; tables and refs are not used.  `from` and `to`
+ * need the same buffer count and block_bytes, and may be the same.  Pairs with
+ * a -1 are skipped; indices out of range are skipped and reported.  A page may
+ * be read many times, but each written page must appear once and not be read.
+ * Errors: INVALID_ARG, CUDA. */
+TQ_API tq_status tq_pages_copy(const tq_handle* h, const tq_pages* from, const tq_pages* to, const int32_t* src,
+                               const int32_t* dst, int64_t n, void* stream);
+
 /* ---- diagnostics -------------------------------------------------------- */
 
 /* Synchronise `stream`, then report and clear the handle's device check word:

@@ -10,9 +10,6 @@ using namespace tqi;
 
 namespace {
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-size_t dtype_size(tq_dtype dt) { return dt == TQ_F32 ? 4 : 2; }
-bool dtype_ok(int dt) { return dt == TQ_F32 || dt == TQ_BF16 || dt == TQ_F16; }
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // Split count for decode.  Work is `pairs` sequences of nchunk chunks; a CTA
@@ -142,14 +139,6 @@ bool make_plan_core(int d, int num_sms, int decode_path, int64_t B, int64_t Hq, 
 bool make_plan(const tq_handle* h, int64_t B, int64_t Hq, int64_t Hkv, int64_t Tmax, DecodePlan* p,
                bool upper_bound, bool equal_len = false) {
     return h && make_plan_core(h->d, h->num_sms, h->decode_path, B, Hq, Hkv, Tmax, p, upper_bound, equal_len);
-}
-
-tq_status cuda_status(cudaError_t e) { return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA; }
-
-bool cache_ok(const tq_handle* h, const tq_cache* c) {
-    return c && c->base && aligned(c->base, 16) && c->B >= 0 && c->Hkv > 0 && c->Tcap > 0 &&
-           c->Tcap % kBlockT == 0 && h &&
-           (!c->block_table || (aligned(c->block_table, 4) && c->pool_blocks > 0 && c->pool_blocks < (1LL << 31)));
 }
 
 tq_status prepare_encode(const tq_handle* h, const void* x, tq_dtype dt, int64_t B, int64_t Hkv, int64_t Tnew,

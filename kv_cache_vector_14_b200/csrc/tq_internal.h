@@ -315,3 +315,16 @@ struct tq_handle {
     int decode_path = 0;              // diagnostics: 0 auto, 1 SIMT, 2 tensor-core uniform splits, 3 tensor-core stream-K
     int first_wait = -1;              // diagnostics: try count of the decode's first ring wait (< 0: full bound)
 };
+
+// Argument checks shared by the C entry points.
+namespace tqi {
+inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline size_t dtype_size(tq_dtype dt) { return dt == TQ_F32 ? 4 : 2; }
+inline bool dtype_ok(int dt) { return dt == TQ_F32 || dt == TQ_BF16 || dt == TQ_F16; }
+inline tq_status cuda_status(cudaError_t e) { return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA; }
+inline bool cache_ok(const tq_handle* h, const tq_cache* c) {
+    return c && c->base && aligned(c->base, 16) && c->B >= 0 && c->Hkv > 0 && c->Tcap > 0 &&
+           c->Tcap % kBlockT == 0 && h &&
+           (!c->block_table || (aligned(c->block_table, 4) && c->pool_blocks > 0 && c->pool_blocks < (1LL << 31)));
+}
+}  // namespace tqi

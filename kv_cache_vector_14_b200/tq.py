@@ -24,7 +24,10 @@ EXPORTED = ("tq_params_host", "tq_init", "tq_destroy", "tq_get_params", "tq_head
             "tq_cache_bytes", "tq_encode_k", "tq_encode_v", "tq_attend_workspace_bytes", "tq_attend_decode",
             "tq_append_attend", "tq_prefill_workspace_bytes", "tq_attend_prefill", "tq_attend_decode_polar",
             "tq_attend_decode_static", "tq_device_status", "tq_set_decode_events", "tq_set_decode_path", "tq_set_wait_limit", "tq_attend_path",
-            "tq_decode_plan", "tq_status_string")
+            "tq_decode_plan", "tq_status_string", "tq_int4_block_bytes", "tq_int4_cache_bytes", "tq_encode_int4",
+            "tq_expand_int4", "tq_attend_int4_workspace_bytes", "tq_attend_int4", "tq_append_attend_int4",
+            "tq_pages_workspace_bytes", "tq_pages_alloc", "tq_pages_fork", "tq_pages_free", "tq_pages_compact",
+            "tq_pages_copy")
 
 
 class TQError(RuntimeError):
@@ -36,6 +39,12 @@ class TQError(RuntimeError):
 class tq_cache(C.Structure):
     _fields_ = [("base", C.c_void_p), ("B", C.c_int64), ("Hkv", C.c_int64), ("Tcap", C.c_int64),
                 ("block_table", C.c_void_p), ("pool_blocks", C.c_int64)]
+
+
+class tq_pages(C.Structure):
+    _fields_ = [("block_table", C.c_void_p), ("refs", C.c_void_p), ("B", C.c_int64), ("Hkv", C.c_int64),
+                ("NB", C.c_int64), ("pool_blocks", C.c_int64), ("n_buffers", C.c_int32),
+                ("buffers", C.POINTER(C.c_void_p)), ("block_bytes", C.POINTER(C.c_int64))]
 
 
 _lock = threading.Lock()
@@ -100,6 +109,31 @@ def lib() -> C.CDLL:
             L.tq_decode_plan.argtypes = [i32, i32, i64, i64, i64, i64, i32, C.POINTER(i32), C.POINTER(i64),
                                          C.POINTER(i64), C.POINTER(i64), C.POINTER(i32)]
             L.tq_decode_plan.restype = st
+            PC, PP, f32, sz = C.POINTER(tq_cache), C.POINTER(tq_pages), C.c_float, C.c_size_t
+            L.tq_int4_block_bytes.argtypes = [i32, i32]
+            L.tq_int4_block_bytes.restype = sz
+            L.tq_int4_cache_bytes.argtypes = [i32, i32, i64, i64, i64]
+            L.tq_int4_cache_bytes.restype = sz
+            for name in ("tq_encode_int4", "tq_expand_int4"):
+                f = getattr(L, name)
+                f.argtypes = [P, i32, P, i32, i64, i64, i64, i64, i64, i64, PC, P, i64, P]
+                f.restype = st
+            L.tq_attend_int4_workspace_bytes.argtypes = [P, i64, i64, i64, i64]
+            L.tq_attend_int4_workspace_bytes.restype = sz
+            L.tq_attend_int4.argtypes = [P, i32, P, i32, i64, i64, i64, PC, PC, P, i64, f32, P, P, sz, P]
+            L.tq_attend_int4.restype = st
+            L.tq_append_attend_int4.argtypes = [P, i32, P, P, i32, i64, i64, i64, i64, PC, PC, P, i64, P, i32, i64,
+                                                f32, P, P, sz, P]
+            L.tq_append_attend_int4.restype = st
+            L.tq_pages_workspace_bytes.argtypes = [PP]
+            L.tq_pages_workspace_bytes.restype = sz
+            L.tq_pages_alloc.argtypes = [P, PP, P, P, P, P, sz, P]
+            L.tq_pages_fork.argtypes = [P, PP, P, P]
+            L.tq_pages_free.argtypes = [P, PP, P, P]
+            L.tq_pages_compact.argtypes = [P, PP, P, P, sz, P]
+            L.tq_pages_copy.argtypes = [P, PP, PP, P, P, i64, P]
+            for name in ("alloc", "fork", "free", "compact", "copy"):
+                getattr(L, "tq_pages_" + name).restype = st
             L.tq_status_string.argtypes = [i32]
             L.tq_status_string.restype = C.c_char_p
             _lib = L
@@ -294,6 +328,189 @@ def tq_attend_prefill(h, q, kc: Cache, vc: Cache, T0: int, out, ws, scale: float
                                    C.byref(vc.struct), T0, float(scale), C.c_void_p(out.data_ptr()),
                                    C.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size(), _stream(stream)),
            "tq_attend_prefill")
+
+
+# ------------------------------------------------------------------ 4-bit caches
+
+def tq_int4_block_bytes(head_dim: int, group: int) -> int:
+    return int(lib().tq_int4_block_bytes(head_dim, group))
+
+
+def tq_int4_cache_bytes(head_dim: int, group: int, B: int, Hkv: int, Tcap: int) -> int:
+    return int(lib().tq_int4_cache_bytes(head_dim, group, B, Hkv, Tcap))
+
+
+class Int4Cache:
+    """A K or V cache of 4-bit codes with a scale and a zero per `group` values,
+    in a PyTorch-owned uint8 device buffer; contiguous or paged as Cache."""
+
+    def __init__(self, head_dim: int, group: int, B: int, Hkv: int, Tcap: int, device="cuda", buf=None,
+                 block_table=None, pool_blocks: int = 0):
+        import torch
+        bb = tq_int4_block_bytes(head_dim, group)
+        if bb == 0 or Tcap <= 0 or Tcap % BLOCK_T:
+            raise ValueError("Tcap must be a positive multiple of 64, head_dim 64, 128 or 256, group 32, 64 or 128 "
+                             "and at most head_dim")
+        if block_table is not None and (block_table.dtype != torch.int32 or not block_table.is_contiguous() or
+                                        tuple(block_table.shape) != (B * Hkv, Tcap // BLOCK_T)):
+            raise ValueError("block_table must be contiguous int32 [B*Hkv, Tcap/64]")
+        nbytes = bb * (pool_blocks if block_table is not None else B * Hkv * (Tcap // BLOCK_T))
+        if buf is not None and (not buf.is_contiguous() or buf.numel() * buf.element_size() < nbytes):
+            raise ValueError(f"buf must be contiguous with at least {nbytes} bytes")
+        self.head_dim, self.group, self.B, self.Hkv, self.Tcap = head_dim, group, B, Hkv, Tcap
+        self.block_bytes, self.nbytes = bb, nbytes
+        self.block_table, self.pool_blocks = block_table, pool_blocks
+        self.buf = buf if buf is not None else torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=device)
+        table = C.c_void_p(block_table.data_ptr()) if block_table is not None else None
+        self.struct = tq_cache(C.c_void_p(self.buf.data_ptr()), B, Hkv, Tcap, table, pool_blocks)
+        self._ref = C.byref(self.struct)
+
+
+def _int32(t, name: str, n: int):
+    """Pointer of a device int32 vector of n elements (None stays None)."""
+    if t is None:
+        return None
+    import torch
+    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int32 with {n} elements")
+    return t.data_ptr()
+
+
+def _same_group(name: str, h, *caches):
+    d = lib().tq_head_dim(h)
+    if any(c.head_dim != d or c.group != caches[0].group for c in caches):
+        raise ValueError(f"{name}: the caches need the handle's head_dim and one group")
+    return d
+
+
+def _int4_copy(name, h, x, cache: Int4Cache, t0: int, pos, stream):
+    d = _same_group(name, h, cache)
+    if x.dim() != 4 or x.shape[3] != d or x.stride(3) != 1:
+        raise ValueError(f"{name}: the vectors must be [B, Hkv, T, {d}] with a contiguous last dim")
+    B, Hkv, T, _ = x.shape
+    sb, sh, st_, _ = x.stride()
+    _check(getattr(lib(), name)(h, cache.group, x.data_ptr(), _dtype_code(x), B, Hkv, T, sb, sh, st_, cache._ref,
+                                _int32(pos, "pos", B), t0, _stream(stream)), name)
+
+
+def tq_encode_int4(h, x, cache: Int4Cache, t0: int = 0, pos=None, stream=None) -> None:
+    """Encode x [B, Hkv, T, d] at positions pos[b] + i (pos: int32 [B]) or t0 + i."""
+    _int4_copy("tq_encode_int4", h, x, cache, t0, pos, stream)
+
+
+def tq_expand_int4(h, cache: Int4Cache, out, t0: int = 0, pos=None, stream=None) -> None:
+    """Read out.shape[2] tokens back into out [B, Hkv, T, d] from positions pos[b] + i or t0 + i."""
+    _int4_copy("tq_expand_int4", h, out, cache, t0, pos, stream)
+
+
+def tq_attend_int4_workspace_bytes(h, B: int, Lq: int, Hq: int, Hkv: int) -> int:
+    return int(lib().tq_attend_int4_workspace_bytes(h, B, Lq, Hq, Hkv))
+
+
+def _int4_queries(name, d, q, out):
+    if q.dim() not in (3, 4) or q.shape[-1] != d or not q.is_contiguous():
+        raise ValueError(f"{name}: q must be contiguous [B, Lq, Hq, {d}] (or [B, Hq, {d}])")
+    if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError(f"{name}: out must be contiguous with q's shape and dtype")
+    return q.shape[0], (q.shape[1] if q.dim() == 4 else 1), q.shape[-2]
+
+
+def tq_attend_int4(h, q, kc: Int4Cache, vc: Int4Cache, out, ws, T: int = 0, seq_lens=None, scale: float = 1.0,
+                   stream=None) -> None:
+    """Attention of q [B, Lq, Hq, d] (or [B, Hq, d]), causal at the end of each
+    sequence of seq_lens[b] (or T) tokens; out has q's shape and dtype."""
+    d = _same_group("tq_attend_int4", h, kc, vc)
+    B, Lq, Hq = _int4_queries("tq_attend_int4", d, q, out)
+    _check(lib().tq_attend_int4(h, kc.group, q.data_ptr(), _dtype_code(q), B, Lq, Hq, kc._ref, vc._ref,
+                                _int32(seq_lens, "seq_lens", B), T, scale, out.data_ptr(), ws.data_ptr(),
+                                ws.numel() * ws.element_size(), _stream(stream)), "tq_attend_int4")
+
+
+def tq_append_attend_int4(h, k_new, v_new, kc: Int4Cache, vc: Int4Cache, q, out, ws, t0: int = 0, pos=None,
+                          scale: float = 1.0, stream=None) -> None:
+    """One step: append k_new/v_new [B, Hkv, Lq, d] (equal dtype and strides) at
+    pos[b] + i or t0 + i, then attend with q [B, Lq, Hq, d] over everything up to them."""
+    d = _same_group("tq_append_attend_int4", h, kc, vc)
+    B, Lq, Hq = _int4_queries("tq_append_attend_int4", d, q, out)
+    if k_new.dim() != 4 or k_new.shape != v_new.shape or k_new.stride() != v_new.stride() or \
+            k_new.dtype != v_new.dtype or k_new.stride(3) != 1 or tuple(k_new.shape) != (B, kc.Hkv, Lq, d):
+        raise ValueError(f"tq_append_attend_int4: k_new, v_new must be [{B}, {kc.Hkv}, {Lq}, {d}] with equal dtype "
+                         "and strides and a contiguous last dim")
+    sb, sh, st_, _ = k_new.stride()
+    _check(lib().tq_append_attend_int4(h, kc.group, k_new.data_ptr(), v_new.data_ptr(), _dtype_code(k_new), Lq, sb, sh,
+                                       st_, kc._ref, vc._ref, _int32(pos, "pos", B), t0, q.data_ptr(), _dtype_code(q),
+                                       Hq, scale, out.data_ptr(), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                       _stream(stream)), "tq_append_attend_int4")
+
+
+# ------------------------------------------------------------------ pages
+
+class Pages:
+    """The pages of paged caches: block_table int32 [B*Hkv, NB] (-1: none), refs
+    int32 [pool blocks], and the pools `buffers` (pairs of a uint8 tensor and the
+    bytes of one page, or Cache / Int4Cache objects) that share the table."""
+
+    def __init__(self, block_table, refs, Hkv: int, buffers):
+        import torch
+        if block_table.dim() != 2 or block_table.dtype != torch.int32 or not block_table.is_contiguous() or \
+                Hkv < 1 or block_table.shape[0] % Hkv:
+            raise ValueError("block_table must be contiguous int32 [B*Hkv, NB]")
+        if refs.dim() != 1 or refs.dtype != torch.int32 or not refs.is_contiguous():
+            raise ValueError("refs must be contiguous int32 [pool blocks]")
+        pairs = []
+        for b in buffers:
+            if isinstance(b, Int4Cache):
+                b = (b.buf, b.block_bytes)
+            elif isinstance(b, Cache):
+                b = (b.buf, tq_block_bytes(b.head_dim, b.is_k))
+            t, nbytes = b
+            if not t.is_contiguous() or t.numel() * t.element_size() < refs.numel() * nbytes:
+                raise ValueError(f"a pool must be contiguous with at least {refs.numel()} pages of {nbytes} bytes")
+            pairs.append((t, int(nbytes)))
+        if len(pairs) > 128:
+            raise ValueError("at most 128 buffers")
+        self.block_table, self.refs, self.Hkv, self.buffers = block_table, refs, Hkv, pairs
+        self.B, self.pool_blocks = block_table.shape[0] // Hkv, refs.numel()
+        self._bases = (C.c_void_p * max(1, len(pairs)))(*[t.data_ptr() for t, _ in pairs])
+        self._bytes = (C.c_int64 * max(1, len(pairs)))(*[n for _, n in pairs])
+        self.struct = tq_pages(block_table.data_ptr(), refs.data_ptr(), self.B, Hkv, block_table.shape[1],
+                               self.pool_blocks, len(pairs), self._bases, self._bytes)
+        self._ref = C.byref(self.struct)
+
+
+def tq_pages_workspace_bytes(pages: Pages) -> int:
+    return int(lib().tq_pages_workspace_bytes(pages._ref))
+
+
+def tq_pages_alloc(h, pages: Pages, lo, hi, info, ws, stream=None) -> None:
+    """Make tokens [lo[b], hi[b]) writable: missing pages are supplied, shared ones
+    copied.  info (int32 [2] or None): free pages left, blocks left without."""
+    _check(lib().tq_pages_alloc(h, pages._ref, _int32(lo, "lo", pages.B), _int32(hi, "hi", pages.B),
+                                _int32(info, "info", 2), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                _stream(stream)), "tq_pages_alloc")
+
+
+def tq_pages_fork(h, pages: Pages, parent, stream=None) -> None:
+    """Every sequence b takes the pages of parent[b] (b: unchanged, -1: none)."""
+    _check(lib().tq_pages_fork(h, pages._ref, _int32(parent, "parent", pages.B), _stream(stream)), "tq_pages_fork")
+
+
+def tq_pages_free(h, pages: Pages, keep, stream=None) -> None:
+    """Release the blocks behind the first keep[b] tokens of every sequence."""
+    _check(lib().tq_pages_free(h, pages._ref, _int32(keep, "keep", pages.B), _stream(stream)), "tq_pages_free")
+
+
+def tq_pages_compact(h, pages: Pages, info, ws, stream=None) -> None:
+    """Move the live pages into the lowest places.  info: free pages, pages moved."""
+    _check(lib().tq_pages_compact(h, pages._ref, _int32(info, "info", 2), ws.data_ptr(),
+                                  ws.numel() * ws.element_size(), _stream(stream)), "tq_pages_compact")
+
+
+def tq_pages_copy(h, src_pages: Pages, dst_pages: Pages, src, dst, stream=None) -> None:
+    """Copy pages src[i] of src_pages' pools to pages dst[i] of dst_pages' (int32)."""
+    n = src.numel()
+    _check(lib().tq_pages_copy(h, src_pages._ref, dst_pages._ref, _int32(src, "src", n), _int32(dst, "dst", n), n,
+                               _stream(stream)), "tq_pages_copy")
 
 
 def tq_device_status(h, stream=None) -> int:
