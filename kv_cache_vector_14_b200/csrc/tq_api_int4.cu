@@ -65,12 +65,13 @@ tq_status copy_common(bool encode, const tq_handle* h, int group, const void* x,
 struct AttendWs {
     size_t off_ml, off_acc, off_split, bytes;
 };
-AttendWs attend_ws(int d, int num_sms) {
+AttendWs attend_ws(int d, int num_sms, int slot_rows) {
     const size_t ctas = num_sms < kInt4MaxCtas ? num_sms : kInt4MaxCtas;
+    const size_t slots = ctas * 2 * slot_rows;
     AttendWs w;
     w.off_ml = 0;
-    w.off_acc = (ctas * 2 * 8 * 2 * 4 + 255) / 256 * 256;
-    w.off_split = w.off_acc + ctas * 2 * 8 * d * 4;
+    w.off_acc = (slots * 2 * 4 + 255) / 256 * 256;
+    w.off_split = w.off_acc + slots * d * 4;
     w.bytes = w.off_split + ctas * sizeof(int4);
     return w;
 }
@@ -81,6 +82,11 @@ bool attend_sizes_ok(int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv) {
     const int64_t G = Hq / Hkv;
     if (Lq * G >= most) return false;
     return Hkv * ((Lq * G + 3) / 4) < most;
+}
+
+cudaError_t launch_any(const tq_handle* h, int group, tq_dtype dt, const Int4AttendArgs& a, cudaStream_t s) {
+    return int4_slot_rows(h->d, dt, a.rows) > 8 ? launch_int4_chunk(h->d, group, dt, a, h->num_sms, s)
+                                                : launch_int4_attend(h->d, group, dt, a, h->num_sms, s);
 }
 
 // Checks of an attention call and its kernel arguments; *empty: nothing to do.
@@ -101,7 +107,7 @@ tq_status prepare_attend(const tq_handle* h, int group, const void* q, tq_dtype 
     }
     if (!q || !out || !ws || !aligned(q, dtype_size(qdt)) || !aligned(out, dtype_size(qdt)) || !aligned(ws, 256))
         return TQ_ERR_INVALID_ARG;
-    const AttendWs w = attend_ws(h->d, h->num_sms);
+    const AttendWs w = attend_ws(h->d, h->num_sms, int4_slot_rows(h->d, qdt, (int)(Lq * (Hq / kc->Hkv))));
     if (ws_bytes < w.bytes) return TQ_ERR_WORKSPACE;
     uint8_t* p = static_cast<uint8_t*>(ws);
     a->q = q;
@@ -126,6 +132,7 @@ tq_status prepare_attend(const tq_handle* h, int group, const void* q, tq_dtype 
     a->split = reinterpret_cast<int4*>(p + w.off_split);
     a->err = h->derr;
     a->first_wait = h->first_wait >= 0 ? h->first_wait : kDefaultWaitLimit;
+    a->vec16 = aligned(q, 16) && aligned(out, 16);
     a->chained = 0;
     return device_ok(h);
 }
@@ -213,7 +220,8 @@ tq_status tq_expand_int4(const tq_handle* h, int group, void* x, tq_dtype dt, in
 
 size_t tq_attend_int4_workspace_bytes(const tq_handle* h, int64_t B, int64_t Lq, int64_t Hq, int64_t Hkv) {
     if (!h || B < 0 || Lq < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv || !attend_sizes_ok(B, Lq, Hq, Hkv)) return 0;
-    return attend_ws(h->d, h->num_sms).bytes;
+    // (the largest over the query types)
+    return attend_ws(h->d, h->num_sms, int4_slot_rows(h->d, TQ_BF16, (int)(Lq * (Hq / Hkv)))).bytes;
 }
 
 tq_status tq_attend_int4(const tq_handle* h, int group, const void* q, tq_dtype qdt, int64_t B, int64_t Lq, int64_t Hq,
@@ -224,7 +232,7 @@ tq_status tq_attend_int4(const tq_handle* h, int group, const void* q, tq_dtype 
     const tq_status r = prepare_attend(h, group, q, qdt, B, Lq, Hq, kc, vc, seq_lens, T, 0, scale, out, ws, ws_bytes, &a,
                                        &empty);
     if (r != TQ_OK || empty) return r;
-    return cuda_status(launch_int4_attend(h->d, group, qdt, a, h->num_sms, static_cast<cudaStream_t>(stream)));
+    return cuda_status(launch_any(h, group, qdt, a, static_cast<cudaStream_t>(stream)));
 }
 
 tq_status tq_append_attend_int4(const tq_handle* h, int group, const void* k_new, const void* v_new, tq_dtype kv_dtype,
@@ -244,7 +252,7 @@ tq_status tq_append_attend_int4(const tq_handle* h, int group, const void* k_new
     a.chained = 1;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t err = launch_int4_encode(h->d, group, kv_dtype, e, h->num_sms, s);
-    if (err == cudaSuccess) err = launch_int4_attend(h->d, group, q_dtype, a, h->num_sms, s);
+    if (err == cudaSuccess) err = launch_any(h, group, q_dtype, a, s);
     return cuda_status(err);
 }
 

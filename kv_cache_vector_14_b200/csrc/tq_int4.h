@@ -59,17 +59,22 @@ struct Int4AttendArgs {
     int G;                    // query heads per kv head
     int rows;                 // Lq G query rows per kv head
     float scale_log2;         // softmax scale * log2(e)
-    float* part_ml;           // [CTA][2][8][2] (reference exponent, sum)
-    float* part_acc;          // [CTA][2][8][d]
+    float* part_ml;           // [CTA][2][rows of a slot][2] (reference exponent, sum)
+    float* part_acc;          // [CTA][2][rows of a slot][d]
     int4* split;              // [CTA] a unit that begins in this CTA and goes on: {sequence, unit, last CTA, 1}
     int* err;
     int first_wait;
+    int vec16;                // q and out start on 16-byte boundaries
     int chained;              // launched as a programmatic dependent of the encode of its newest tokens
 };
 constexpr int kInt4MaxCtas = 256;
+// Rows of a partial slot, by which a call's kernel is known: 8 the split kernel
+// (tq_int4_attend.cu), 128 and 256 the chunk kernel (tq_int4_chunk.cu).
+int int4_slot_rows(int d, tq_dtype dt, int rows);
 
 cudaError_t launch_int4_encode(int d, int group, tq_dtype dt, const Int4CopyArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_int4_expand(int d, int group, tq_dtype dt, const Int4CopyArgs& a, int num_sms, cudaStream_t s);
 cudaError_t launch_int4_attend(int d, int group, tq_dtype dt, const Int4AttendArgs& a, int num_sms, cudaStream_t s);
+cudaError_t launch_int4_chunk(int d, int group, tq_dtype dt, const Int4AttendArgs& a, int num_sms, cudaStream_t s);
 
 }  // namespace tqi

@@ -36,6 +36,7 @@
 
 #include "tq_frag.cuh"
 #include "tq_int4.h"
+#include "tq_int4_combine.cuh"
 
 namespace tqi {
 namespace {
@@ -151,6 +152,10 @@ struct Words {
 // nibbles r (and r + 4) of a word as two fp16 subnormals: c 2^-24 for even r, 16 c 2^-24 for odd
 __device__ __forceinline__ uint32_t pick(uint32_t w, uint32_t w8, int r) {
     return (r < 2 ? w : w8) & ((r & 1) ? 0x00f000f0u : 0x000f000fu);
+}
+// the same with 15 - c in the high half (an odd token's value; see the kernel's value step)
+__device__ __forceinline__ uint32_t pick_odd(uint32_t w, uint32_t w8, int r) {
+    return pick(w, w8, r) ^ ((r & 1) ? 0x00f00000u : 0x000f0000u);
 }
 
 template <int D, int GRP, int NT, int DT>
@@ -507,8 +512,18 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
                     lsum[nt] += pA[nt] + pB[nt];
                 }
                 // ---- values: O^T += Cv^T (p vs); lane quarter t takes tokens 2t, 2t + 1 (+ 8), the
-                // odd one first where t >= 2 (bank conflicts)
+                // odd one first where t >= 2 (bank conflicts).  An odd token enters as
+                // p (vz + 15 vs) - p vs (15 - c): codes are all positive and a long flat softmax
+                // would sum them to many times the result, with the tensor core's truncated
+                // additions (relative error against 64 bits at 4133 tokens 7e-5; this way 7e-7)
                 const int par = tq4 >> 1;
+                const float c15 = (gr & 1) ? 15.f : 0.f;      // this lane's tokens are odd
+                float qA[NT], qB[NT];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    qA[nt] = (gr & 1) ? -pA[nt] : pA[nt];
+                    qB[nt] = (gr & 1) ? -pB[nt] : pB[nt];
+                }
                 const uint32_t sel_lo = par ? 0x1054u : 0x5410u, sel_hi = par ? 0x3276u : 0x7632u;
                 const int v0 = kt * 16 + 2 * tq4 + par, v1 = kt * 16 + 2 * tq4 + 1 - par;
 #pragma unroll
@@ -516,8 +531,8 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
                     uint32_t pb[NT][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float wA = pA[nt] * vA[gam].x, wB = pB[nt] * vB[gam].x;
-                        float yA = vA[gam].y, yB = vB[gam].y;
+                        float wA = qA[nt] * vA[gam].x, wB = qB[nt] * vB[gam].x;
+                        float yA = fmaf(vA[gam].x, c15, vA[gam].y), yB = fmaf(vB[gam].x, c15, vB[gam].y);
                         if constexpr (PARTIAL) {              // p = 0 there, but the pair may be anything
                             if (!okA[nt]) wA = yA = 0.f;
                             if (!okB[nt]) wB = yB = 0.f;
@@ -544,7 +559,7 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
                             const uint32_t x8 = x >> 8, y8 = y >> 8;
 #pragma unroll
                             for (int r = 0; r < 4; r += 2) {
-                                const uint32_t va[4] = {pick(x, x8, r), pick(x, x8, r + 1), pick(y, y8, r), pick(y, y8, r + 1)};
+                                const uint32_t va[4] = {pick_odd(x, x8, r), pick_odd(x, x8, r + 1), pick_odd(y, y8, r), pick_odd(y, y8, r + 1)};
                                 const int mt = gam * (GRP / 16) + k * 4 + half * 2 + (r >> 1);
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][mt], va, pb[nt][0], pb[nt][1]);
@@ -601,7 +616,7 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
         __syncthreads();
         const bool whole = us >= lo && ue <= hi;
         // a cut unit's partial: slot 1 where it begins in this CTA, else slot 0
-        const int64_t slot = (2 * c + (us >= lo ? 1 : 0)) * 8;
+        const int64_t slot = (2 * c + (us >= lo ? 1 : 0)) * ROWS;
         for (int idx = tid; idx < nrow * D; idx += NW * 32) {
             const int r = idx / D, j = idx % D;
             float M = -INFINITY;
@@ -636,36 +651,6 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
     pdl_trigger();
 }
 
-// Merges the partials of a unit cut by CTA borders: block (c, r) row r of the unit that
-// begins in CTA c, thread j coordinate j.
-template <int D, int DT>
-__global__ void __launch_bounds__(D) tq_int4_combine_kernel(const Int4AttendArgs a, int rows_per_unit) {
-    const int c = blockIdx.x, r = blockIdx.y, j = threadIdx.x;
-    pdl_wait();
-    const int4 s = a.split[c];
-    if (!s.w) return;
-    const int rgroups = (a.rows + rows_per_unit - 1) / rows_per_unit;
-    const int kv = s.y / rgroups, row = (s.y - kv * rgroups) * rows_per_unit + r;
-    if (row >= a.rows) return;
-    // the unit's partials: slot 1 of CTA c, slot 0 of CTAs c + 1 .. s.z
-    auto at = [&](int k) -> int64_t { return k == 0 ? (2 * (int64_t)c + 1) * 8 + r : (2 * ((int64_t)c + k)) * 8 + r; };
-    const int n = s.z - c + 1;
-    float M = -INFINITY;
-    for (int k = 0; k < n; ++k) M = fmaxf(M, a.part_ml[at(k) * 2]);
-    float L = 0.f, A = 0.f;
-    if (M != -INFINITY) {
-#pragma unroll 4
-        for (int k = 0; k < n; ++k) {
-            const float m = a.part_ml[at(k) * 2];
-            const float f = fast_exp2(m - M);                 // 0 where m is -inf
-            L = fmaf(f, a.part_ml[at(k) * 2 + 1], L);
-            A = fmaf(f, a.part_acc[at(k) * D + j], A);
-        }
-    }
-    const int64_t qi = row / a.G, g = row - qi * a.G;
-    store_elem<DT>(a.out, ((s.x * a.Lq + qi) * a.Hq + (int64_t)kv * a.G + g) * D + j, M == -INFINITY ? 0.f : A / L);
-}
-
 template <int D, int GRP, int NT, int DT>
 cudaError_t launch_t(const Int4AttendArgs& a, int num_sms, cudaStream_t s) {
     using S = Shape<D, GRP, NT>;
@@ -679,7 +664,7 @@ cudaError_t launch_t(const Int4AttendArgs& a, int num_sms, cudaStream_t s) {
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) return e;
-    return launch_pdl(tq_int4_combine_kernel<D, DT>, dim3(ctas, S::kRows), dim3(D), 0, s, a, S::kRows);
+    return launch_int4_combine<D, DT>(a, S::kRows, false, ctas, s);
 }
 template <int D, int GRP>
 cudaError_t launch_g(tq_dtype dt, const Int4AttendArgs& a, int num_sms, cudaStream_t s) {

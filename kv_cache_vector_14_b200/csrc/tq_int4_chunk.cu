@@ -1,0 +1,808 @@
+// Attention of many query rows over the 4-bit cache (prefill chunks, speculative
+// tokens) on the 5th-generation tensor cores (tcgen05, accumulators, query
+// operand and softmax weights in tensor memory), head_dim 64 and 128, for sm_100a.
+//
+// Mathematics as in tq_int4_attend.cu.  A unit is 128 MT query rows (query i,
+// head g: row i G + g) of one kv head; its tokens come in tiles of 64, one cache
+// block.  A tile is expanded once into shared memory and serves all rows:
+//   S[128 rows][64 tok] = Q K^T      (A: Q in tensor memory, B: K, K-major)
+//   O[128 rows][D]     += P V        (A: P in tensor memory over S, B: V, MN-major)
+// The expanded values zero + scale c are rounded to fp16, bf16 and fp16 queries
+// enter exactly (scaled by a power of two per row), P is fp16.  For bf16 that is
+// one product each (NL = 1): those roundings are 2^-11 relative and the output's
+// own is 2^-8.  For fp16 and fp32 they would show, so K, V and P (and fp32 Q) are
+// kept as fp16 hi + lo (NL = 2, 22 bits) and three products are summed, hi hi +
+// lo hi + hi lo, in the same fp32 accumulator.
+//
+// Warp roles: warps 0-3 and 4-7 are two softmax streams, each with its own O
+// accumulator, so that neither waits for the other; a thread owns a row.  With
+// MT = 2 they are the two row tiles of the unit, and an expanded tile serves 256
+// rows; with MT = 1 (few rows, or fp32, whose query limbs leave no tensor memory)
+// they take the even and the odd tiles and are merged at the unit's end.  Warps
+// 8-11 copy blocks (ring of bulk copies) and expand them; warp 12 issues the mma
+// (one thread): while one stream's softmax works, the tensor core runs the other
+// stream's products.  The mma of one thread run in issue order, so a stream's next
+// S cannot overwrite P before its O has read it, and a completed S says that the
+// stream's last O is done, which is when it may be rescaled (the reference
+// exponent moves only when it is exceeded by 2^8).
+//
+// Work: the units' tiles (each unit only as far as its last row sees) laid end
+// to end, shared out evenly over one CTA per SM on the device, cut units merged
+// by the combine kernel, as in tq_int4_attend.cu.
+//
+// NaN: a value group with a non-finite pair is expanded as zeros and its token
+// marked; rows that see the token get NaN in that group at the end.  So a NaN
+// does not reach the rows for which it is masked, as a product 0 NaN would.
+#include "tq_frag.cuh"
+#include "tq_int4.h"
+#include "tq_int4_combine.cuh"
+#include "tq_tc.cuh"
+
+namespace tqi {
+namespace {
+
+constexpr int kT = 64;                    // tokens per tile
+constexpr int kSoft = 256;                // softmax threads
+constexpr int kProd = 128;                // producer threads
+constexpr int kThreads = kSoft + kProd + 32;
+constexpr float kRoom = 7.f, kLazy = 8.f; // P is kept below 2^15 (fp16 holds 65504)
+
+template <int D, int GRP, int NL>
+struct Ch {
+    static constexpr int kNG = D / GRP;
+    static constexpr int kBlockB = 64 * (D / 2 + 4 * kNG);
+    static constexpr int kTile = kT * D * 2;                  // one fp16 operand of a tile
+    static constexpr int kBuf = 2 * NL * kTile;               // K limbs, V limbs
+    static constexpr int kBufs = NL == 1 ? 3 : 2;
+    static constexpr int kRing = 3;
+    static constexpr int kStage = 2 * kBlockB;
+    static constexpr int kOffRing = kBufs * kBuf;
+    static constexpr int kOffBar = kOffRing + kRing * kStage;
+    static constexpr int kOffBad = kOffBar + 24 * 8;          // per buffer: token marks [64], any mark
+    static constexpr int kOffXch = kOffBad + kBufs * 80 * 4;  // [2][3][128]: reference, sum, NaN groups
+    static constexpr int kOffScan = kOffXch + 6 * 128 * 4;    // [kThreads / 32 + 3] int64
+    static constexpr int kOffMisc = kOffScan + (kThreads / 32 + 3) * 8;
+    static constexpr int kSmem = kOffMisc + 16 + 1024;        // + slack to align the base
+    static_assert(kOffRing % 16 == 0 && kOffBar % 8 == 0 && kOffScan % 8 == 0, "alignment");
+    static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
+};
+// tensor memory columns
+template <int D, int QL, int MT>
+struct Tm {
+    static constexpr int kQ = 0;                              // MT x QL x D/2
+    static constexpr int kX = MT * QL * D / 2;                // S / P of stream x at kX + 64 x
+    static constexpr int kO = kX + 128;                       // O of stream x at kO + D x
+    static_assert(kO + 2 * D <= 512, "tensor memory");
+};
+
+enum : int {
+    kBarRing = 0,      // [3] raw blocks of a stage in shared memory (copy bytes)
+    kBarReady = 3,     // [3] operands of a buffer built (kProd arrivals)
+    kBarFree = 6,      // [3] operands of a buffer read (commit)
+    kBarS = 9,         // [2] S of stream x computed (commit)
+    kBarP = 11,        // [2] P of stream x written (128 arrivals)
+    kBarSeg = 13,      // O of a segment complete (commit)
+    kBarQ = 14,        // query operand written (256 arrivals)
+    kBarDrain = 15,    // every mma done (commit, at exit)
+};
+
+// tokens that the last row of row tile rt sees, and the tiles they take (at least one)
+__device__ __forceinline__ int64_t chunk_len(const Int4AttendArgs& a, int64_t b) {
+    const int64_t n = (a.lens ? (int64_t)__ldg(a.lens + b) : a.T) + a.add;
+    return n < 0 ? 0 : (n > a.Tcap ? a.Tcap : n);
+}
+template <int ROWS>
+__device__ __forceinline__ int unit_tiles(const Int4AttendArgs& a, int64_t n, int rt) {
+    const int64_t last = (int64_t)rt * ROWS + ROWS - 1 < a.rows ? (int64_t)rt * ROWS + ROWS - 1 : a.rows - 1;
+    const int64_t sees = n - a.Lq + 1 + last / a.G;
+    const int64_t t = (sees + kT - 1) / kT;
+    return t > 1 ? (int)t : 1;
+}
+
+// Walks the flattened tiles: (sequence, row tile) pair, kv head, tile.
+template <int ROWS>
+struct Walk {
+    int64_t n;         // tokens of the sequence
+    int b, rt, kv, k, nt, R;
+    __device__ void load(const Int4AttendArgs& a) {
+        n = chunk_len(a, b);
+        nt = unit_tiles<ROWS>(a, n, rt);
+    }
+    __device__ void next(const Int4AttendArgs& a) {
+        if (++k < nt) return;
+        k = 0;
+        if (++kv < (int)a.Hkv) return;
+        kv = 0;
+        if (++rt == R) {
+            rt = 0;
+            if (++b == (int)a.B) { b = 0; return; }           // behind the last tile: not used
+        }
+        load(a);
+    }
+};
+
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+    return __all_sync(kFull, mbar_wait_bounded(bar, parity));
+}
+// barrier over the softmax threads that ORs v
+__device__ __forceinline__ bool soft_or(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "n"(kSoft)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ bool prod_or(bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 2, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "n"(kProd)
+        : "memory");
+    return r != 0;
+}
+template <int DT>
+__device__ __forceinline__ float q_elem(const void* p, int64_t i) {
+    if constexpr (DT == TQ_F32) return __ldg(static_cast<const float*>(p) + i);
+    else if constexpr (DT == TQ_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+    else return __half2float(static_cast<const __half*>(p)[i]);
+}
+template <int DT>
+__device__ __forceinline__ void put_elem(void* p, int64_t i, float x) {
+    if constexpr (DT == TQ_F32) static_cast<float*>(p)[i] = x;
+    else if constexpr (DT == TQ_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
+    else static_cast<__half*>(p)[i] = __float2half_rn(x);
+}
+// Operand position p (0 .. 7) of a word's eight values holds value word_value(p): the
+// order in which masks pick nibbles r and r + 4
+__host__ __device__ constexpr int word_value(int p) { return (p >> 1) + 4 * (p & 1); }
+
+__device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
+
+// the eight values of word w, zero + scale c, as four fp16 pairs (hi; with NL = 2 lo too)
+template <int NL>
+__device__ __forceinline__ void expand_word(uint32_t w, __half2 s2, __half2 z2, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+    const uint32_t w8 = w >> 8;
+    const __half2 m1024 = as_h2(0xe400e400u), sixteenth = as_h2(0x2c002c00u), m64 = as_h2(0xd400d400u);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const uint32_t v = r < 2 ? w : w8;
+        // 1024 + c (or 1024 + 16 c) as fp16, then c exactly, then one rounding of zero + scale c
+        const __half2 c = (r & 1) ? __hfma2(as_h2((v & 0x00f000f0u) | 0x64006400u), sixteenth, m64)
+                                  : __hadd2(as_h2((v & 0x000f000fu) | 0x64006400u), m1024);
+        const __half2 h = __hfma2(c, s2, z2);
+        hi[r] = h2_bits(h);
+        if constexpr (NL == 2) {
+            const float2 cf = __half22float2(c), hf = __half22float2(h);
+            const float s = __low2float(s2), z = __low2float(z2);
+            lo[r] = h2_bits(__floats2half2_rn(fmaf(cf.x, s, z) - hf.x, fmaf(cf.y, s, z) - hf.y));
+        }
+    }
+}
+
+// packed fp32 pairs
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// N consecutive elements of a row as floats; vec: the row is 16-byte aligned
+template <int DT, int N>
+__device__ __forceinline__ void load_row(const void* p, int64_t at, bool vec, float (&v)[N]) {
+    constexpr int kE = DT == TQ_F32 ? 4 : 2;
+    if (vec) {
+        const uint4* s = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * kE);
+#pragma unroll
+        for (int i = 0; i < N * kE / 16; ++i) {
+            const uint4 u = __ldg(s + i);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (DT == TQ_F32) {
+                    v[4 * i + k] = __uint_as_float(w[k]);
+                } else if constexpr (DT == TQ_BF16) {
+                    v[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
+                    v[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+                } else {
+                    const float2 f = __half22float2(as_h2(w[k]));
+                    v[8 * i + 2 * k] = f.x;
+                    v[8 * i + 2 * k + 1] = f.y;
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = q_elem<DT>(p, at + i);
+    }
+}
+// eight consecutive outputs
+template <int DT>
+__device__ __forceinline__ void store8(void* p, int64_t at, bool vec, const float (&v)[8]) {
+    if (!vec) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) put_elem<DT>(p, at + i, v[i]);
+    } else if constexpr (DT == TQ_F32) {
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
+        o[0] = make_float4(v[0], v[1], v[2], v[3]);
+        o[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (DT == TQ_BF16) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+                w[k] = *reinterpret_cast<const uint32_t*>(&h);
+            } else {
+                w[k] = h2_bits(__floats2half2_rn(v[2 * k], v[2 * k + 1]));
+            }
+        }
+        *reinterpret_cast<uint4*>(static_cast<char*>(p) + at * 2) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+template <int D, int GRP, int DT, int MT>
+__global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid_constant__ Int4AttendArgs a) {
+    constexpr int NL = DT == TQ_BF16 ? 1 : 2;                 // limbs of K, V and P
+    constexpr int QL = DT == TQ_F32 ? 2 : 1;                  // limbs of Q
+    constexpr int ROWS = 128 * MT;
+    using C = Ch<D, GRP, NL>;
+    using M = Tm<D, QL, MT>;
+    using W = Walk<ROWS>;
+    constexpr int NG = C::kNG;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw = smem_u32(smem_raw);
+    uint8_t* sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+    const uint32_t sbase = smem_u32(sm);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + C::kOffBar);
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    int64_t* sScan = reinterpret_cast<int64_t*>(sm + C::kOffScan);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + C::kOffMisc);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    constexpr int kWarps = kThreads / 32;
+
+    if (tid == 0) {
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(bar(kBarRing + i), 1);
+            mbar_init(bar(kBarReady + i), kProd);
+            mbar_init(bar(kBarFree + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kBarS + i), 1);
+            mbar_init(bar(kBarP + i), 128);
+        }
+        mbar_init(bar(kBarSeg), 1);
+        mbar_init(bar(kBarQ), kSoft);
+        mbar_init(bar(kBarDrain), 1);
+        fence_mbar_init();
+    }
+    if (warp == 0) {
+        tc_alloc(smem_u32(tmem_slot), 512);
+        tc_relinquish();
+    }
+    if (a.chained) pdl_wait();
+
+    // ---------------- this CTA's share of the tiles: pairs (sequence, row tile) in order, each
+    // Hkv units of unit_tiles tiles; a scan over runs of pairs finds the place
+    const int R = (a.rows + ROWS - 1) / ROWS;
+    const int64_t pairs = a.B * R, per = (pairs + kThreads - 1) / kThreads;
+    const int64_t p0 = tid * per < pairs ? tid * per : pairs, p1 = p0 + per < pairs ? p0 + per : pairs;
+    auto span_of = [&](int64_t p) -> int64_t {
+        const int64_t b = p / R;
+        return (int64_t)unit_tiles<ROWS>(a, chunk_len(a, b), (int)(p - b * R)) * a.Hkv;
+    };
+    int64_t mine = 0;
+    for (int64_t p = p0; p < p1; ++p) mine += span_of(p);
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += x;
+    }
+    if (lane == 31) sScan[warp] = incl;
+    tc_fence_before();
+    __syncthreads();                       // (also: mbarriers and tensor memory are set up)
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    int64_t before = 0, N = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += sScan[w];
+        N += sScan[w];
+    }
+    const int64_t c = blockIdx.x, nC = N < gridDim.x ? N : gridDim.x;
+    const int64_t lo = c < nC ? c * N / nC : 0;
+    {
+        int64_t base = before + incl - mine;
+        if (base <= lo && lo < base + mine)
+            for (int64_t p = p0; p < p1; ++p) {
+                const int64_t span = span_of(p);
+                if (lo < base + span) {
+                    sScan[kWarps] = p;
+                    sScan[kWarps + 1] = lo - base;
+                    break;
+                }
+                base += span;
+            }
+    }
+    __syncthreads();
+    if (tid == 0) a.split[c] = make_int4(0, 0, 0, 0);
+    const int J = c < nC ? (int)((c + 1) * N / nC - lo) : 0;  // tiles of this CTA
+    W w0;
+    w0.R = R;
+    w0.b = (int)(sScan[kWarps] / R);
+    w0.rt = (int)(sScan[kWarps] - (int64_t)w0.b * R);
+    w0.load(a);
+    w0.kv = (int)(sScan[kWarps + 1] / w0.nt);
+    w0.k = (int)(sScan[kWarps + 1] - (int64_t)w0.kv * w0.nt);
+
+    bool failed = false;
+    if (warp < 8) {
+        // ======================================== softmax: stream x, thread = row r of its tile
+        const int x = warp >> 2, r = tid & 127;
+        const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        float* xch = reinterpret_cast<float*>(sm + C::kOffXch);
+        W w = w0;
+        int seg = 0, nS = 0;                                  // segments, S of this stream so far
+        for (int j = 0; j < J; ++seg) {
+            // ---- a segment: tiles j .. j1 - 1 of one unit
+            const int k0 = w.k, left = w.nt - w.k;
+            const int j1 = j + left < J ? j + left : J;
+            const int ur = MT == 2 ? 128 * x + r : r;         // row of the unit
+            const int64_t grow = (int64_t)w.rt * ROWS + ur;
+            const bool rvalid = grow < a.rows;
+            const int64_t qi = rvalid ? grow / a.G : 0, qg = rvalid ? grow - qi * a.G : 0;
+            const int64_t qrow = ((int64_t)w.b * a.Lq + qi) * a.Hq + (int64_t)w.kv * a.G + qg;
+            const int64_t lim = rvalid ? w.n - a.Lq + 1 + qi : 0;
+            // query operand: the row scaled by a power of two (largest element in [2^14, 2^15));
+            // with MT = 1 each stream does half of the columns.  Column cc holds positions 2 cc, 2 cc + 1
+            float fr;
+            {
+                constexpr int NQ = MT == 2 ? D : D / 2;
+                const int q0 = MT == 2 ? 0 : x * (D / 2);
+                float mx = 0.f;
+                if (rvalid) {
+#pragma unroll
+                    for (int e0 = 0; e0 < NQ; e0 += 32) {
+                        float v[32];
+                        load_row<DT, 32>(a.q, qrow * D + q0 + e0, a.vec16, v);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, fabsf(v[e]));
+                    }
+                }
+                if constexpr (MT == 1) {
+                    xch[x * 128 + r] = mx;
+                    soft_or(false);
+                    mx = fmaxf(mx, xch[(x ^ 1) * 128 + r]);
+                    soft_or(false);
+                }
+                int ex = mx > 0.f ? ilogbf(mx) : 0;
+                ex = ex < -100 ? -100 : ex;
+                const float f = mx <= 3.4e38f ? exp2f((float)(14 - ex)) : 1.f;
+                const float fs = a.scale_log2 < 0.f ? -f : f;
+                fr = fmaxf(fabsf(a.scale_log2) / f, 1e-37f);  // (above zero: a masked -inf stays one)
+                const uint32_t tq = tl + M::kQ + (MT == 2 ? x * QL * (D / 2) : x * (D / 4));
+#pragma unroll 1
+                for (int c0 = 0; c0 < NQ / 2; c0 += 16) {
+                    uint32_t qh[16], qlo[16];
+                    float v[32];
+                    if (rvalid) {
+                        load_row<DT, 32>(a.q, qrow * D + q0 + 2 * c0, a.vec16, v);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                    }
+#pragma unroll
+                    for (int cc = 0; cc < 16; ++cc) {
+                        const int e = 2 * cc & ~7;
+                        split_hilo(v[e + word_value(2 * cc & 7)] * fs, v[e + word_value((2 * cc & 7) + 1)] * fs, qh[cc], qlo[cc]);
+                    }
+                    tc_st16(tq + c0, qh);
+                    if constexpr (QL == 2) tc_st16(tq + D / 2 + c0, qlo);
+                }
+                tc_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(kBarQ));
+            }
+            float mref = -INFINITY, lsum = 0.f;
+            uint32_t nanmask = 0;
+            bool any = false;                                  // this stream has an O
+            const uint32_t tx = tl + M::kX + 64 * x;
+            const uint64_t fr2 = pack2(fr, fr);
+            for (int jj = MT == 2 ? j : j + ((j & 1) ^ x); jj < j1 && !failed; jj += 3 - MT) {
+                const int k = k0 + (jj - j);
+                if (!warp_wait(bar(kBarS + x), (uint32_t)(nS & 1))) { failed = true; break; }
+                ++nS;
+                tc_fence_after();
+                uint32_t sv[64];
+                tc_ld64(tx, sv);
+                const int64_t tok0 = (int64_t)k * kT;
+                const int vis = lim - tok0 >= kT ? kT : (int)(lim > tok0 ? lim - tok0 : 0);
+                if (vis < kT) {
+#pragma unroll
+                    for (int t = 0; t < kT; ++t)
+                        if (t >= vis) sv[t] = 0xff800000u;
+                }
+                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int t = 0; t < kT; t += 8)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        mx4[q] = fmaxf(mx4[q], fmaxf(__uint_as_float(sv[t + 2 * q]), __uint_as_float(sv[t + 2 * q + 1])));
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fr;
+                // move the reference when it is exceeded by 2^kLazy; O is rescaled by whole warps
+                const bool move = mx - kRoom - kLazy > mref;
+                if (__any_sync(kFull, move)) {
+                    float f = 1.f;
+                    if (move) {
+                        f = mref == -INFINITY ? 0.f : fast_exp2(mref - (mx - kRoom));
+                        mref = mx - kRoom;
+                        lsum *= f;
+                    }
+                    if (any) {
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 16) {
+                            uint32_t ov[16];
+                            tc_ld16(tl + M::kO + D * x + c0, ov);
+#pragma unroll
+                            for (int cc = 0; cc < 16; ++cc) ov[cc] = __float_as_uint(__uint_as_float(ov[cc]) * f);
+                            tc_st16(tl + M::kO + D * x + c0, ov);
+                        }
+                    }
+                }
+                any = true;
+                const float m = mref == -INFINITY ? 0.f : mref;
+                const uint64_t m2 = pack2(-m, -m);
+                uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {               // 32 tokens at a time: fewer registers
+                    uint32_t ph[16], pl[16];
+#pragma unroll
+                    for (int t = 0; t < 32; t += 2) {
+                        float e0, e1;
+                        unpack2(fma2(pack2(__uint_as_float(sv[32 * hf + t]), __uint_as_float(sv[32 * hf + t + 1])), fr2, m2),
+                                e0, e1);
+                        e0 = fast_exp2(e0);
+                        e1 = fast_exp2(e1);
+                        sum2[(t >> 1) & 1] = add2(sum2[(t >> 1) & 1], pack2(e0, e1));
+                        if constexpr (NL == 2) split_hilo(e0, e1, ph[t >> 1], pl[t >> 1]);
+                        else ph[t >> 1] = h2_bits(__floats2half2_rn(e0, e1));
+                    }
+                    tc_st16(tx + 16 * hf, ph);
+                    if constexpr (NL == 2) tc_st16(tx + 32 + 16 * hf, pl);
+                }
+                float s0, s1;
+                unpack2(add2(sum2[0], sum2[1]), s0, s1);
+                lsum += s0 + s1;
+                tc_wait_st();
+                // tokens marked by the producers
+                const uint32_t* bad = reinterpret_cast<const uint32_t*>(sm + C::kOffBad) + (jj % C::kBufs) * 80;
+                if (!warp_wait(bar(kBarReady + jj % C::kBufs), (uint32_t)((jj / C::kBufs) & 1))) { failed = true; break; }
+                if (bad[64])
+                    for (int t = 0; t < vis; ++t) nanmask |= bad[t];
+                tc_fence_before();
+                mbar_arrive(bar(kBarP + x));
+            }
+            // ---- the segment's end
+            if (!failed && !warp_wait(bar(kBarSeg), (uint32_t)(seg & 1))) failed = true;
+            tc_fence_after();
+            if (!any) mref = -INFINITY;
+            if (lsum != lsum && mref == -INFINITY) mref = 0.f;   // nothing but NaN scores
+            xch[(x * 3 + 0) * 128 + r] = mref;
+            xch[(x * 3 + 1) * 128 + r] = lsum;
+            xch[(x * 3 + 2) * 128 + r] = __uint_as_float(nanmask);
+            if (soft_or(failed)) failed = true;
+            const bool begins = k0 == 0, ends = j1 - j == left, whole = begins && ends;
+            const int64_t slot = (2 * c + (begins ? 1 : 0)) * ROWS + ur;
+            // MT = 1: both streams' results, each stream half of the coordinates
+            float m0 = mref, m1 = -INFINITY, l0 = lsum, l1 = 0.f;
+            uint32_t bad = nanmask;
+            if constexpr (MT == 1) {
+                m0 = xch[r];
+                m1 = xch[3 * 128 + r];
+                l0 = xch[128 + r];
+                l1 = xch[4 * 128 + r];
+                bad = __float_as_uint(xch[2 * 128 + r]) | __float_as_uint(xch[5 * 128 + r]);
+            }
+            const float mm = failed ? -INFINITY : fmaxf(m0, m1);
+            const float f0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - mm), f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - mm);
+            const float L = mm == -INFINITY ? 0.f : (f0 == 0.f ? 0.f : f0 * l0) + (f1 == 0.f ? 0.f : f1 * l1);
+            const float inv = whole && mm != -INFINITY ? 1.f / L : 1.f;
+            constexpr int kCols = MT == 2 ? D : D / 2;
+#pragma unroll 1
+            for (int c0 = 0; c0 < kCols; c0 += 32) {
+                const int col = MT == 2 ? c0 : x * (D / 2) + c0;
+                uint32_t o0[32], o1[32];
+                tc_ld32(tl + M::kO + (MT == 2 ? D * x : 0) + col, o0);
+                if constexpr (MT == 1) tc_ld32(tl + M::kO + D + col, o1);
+                const bool poison = (bad >> (col / GRP)) & 1u; // (a run of 32 lies in one group)
+                if (!rvalid) continue;
+                float v[32];
+#pragma unroll
+                for (int cc = 0; cc < 32; ++cc) {
+                    float y = 0.f;
+                    if (mm != -INFINITY) {
+                        if (f0 != 0.f) y = __uint_as_float(o0[cc]) * f0;
+                        if constexpr (MT == 1)
+                            if (f1 != 0.f) y = fmaf(__uint_as_float(o1[cc]), f1, y);
+                        if (poison) y = __uint_as_float(0x7fc00000u);
+                    }
+                    v[(cc & ~7) + word_value(cc & 7)] = y * inv;
+                }
+#pragma unroll
+                for (int i = 0; i < 32; i += 8) {
+                    const float u[8] = {v[i], v[i + 1], v[i + 2], v[i + 3], v[i + 4], v[i + 5], v[i + 6], v[i + 7]};
+                    if (whole) store8<DT>(a.out, qrow * D + col + i, a.vec16, u);
+                    else store8<TQ_F32>(a.part_acc, slot * D + col + i, true, u);
+                }
+            }
+            if (rvalid && !whole && (MT == 2 || x == 0)) {
+                a.part_ml[2 * slot] = mm;
+                a.part_ml[2 * slot + 1] = L;
+            }
+            // a unit that begins here and goes on: up to the CTA of its last tile
+            if (tid == 0 && begins && !ends) {
+                const int64_t end = lo + j + left;             // (flattened index behind its last tile)
+                a.split[c] = make_int4(w.b, w.rt * (int)a.Hkv + w.kv, (int)((end * nC - 1) / N), 1);
+            }
+            // the next segment's queries and exchange overwrite what was read here
+            tc_fence_before();
+            soft_or(false);
+            tc_fence_after();
+            w.k = w.nt - 1;                                    // on to the next unit
+            w.next(a);
+            j = j1;
+        }
+        if (failed) atomicExch(a.err, 1);
+    } else if (warp < 12) {
+        // ======================================== producers: thread = token `tau` (and tau + 32)
+        // of piece cp (32 values; D = 64: two warps share a piece), K and V
+        const int pt = tid - kSoft;
+        W wi = w0, w = w0;
+        auto issue = [&](int j) {
+            uint8_t* stg = sm + C::kOffRing + (j % C::kRing) * C::kStage;
+            const uint32_t br = bar(kBarRing + j % C::kRing);
+            const int64_t bh = (int64_t)wi.b * a.Hkv + wi.kv;
+            const bool some = wi.n > 0;
+            const int64_t kb = some ? cache_block(a.ktable, a.kpool, a.NB, bh, wi.k, a.err) : 0;
+            const int64_t vb = some ? cache_block(a.vtable, a.vpool, a.NB, bh, wi.k, a.err) : 0;
+            mbar_expect_tx(br, (uint32_t)C::kStage);
+            bulk_g2s(smem_u32(stg), a.kc + (kb >= 0 ? kb : 0) * C::kBlockB, C::kBlockB, br);
+            bulk_g2s(smem_u32(stg + C::kBlockB), a.vc + (vb >= 0 ? vb : 0) * C::kBlockB, C::kBlockB, br);
+        };
+        int issued = 0;
+        if (pt == 0) {
+            asm volatile("fence.proxy.async;" ::: "memory");
+            for (; issued < C::kRing && issued < J; ++issued) {
+                issue(issued);
+                wi.next(a);
+            }
+        }
+        constexpr int kPieces = D / 32, kPer = kT * kPieces / kProd;     // items per side and thread
+        const int cp = (pt >> 5) % kPieces, tau0 = lane + 32 * ((pt >> 5) / kPieces);
+        const int src = tau0 * (D / 2) + ((cp * 16) ^ int4_swizzle(D, tau0));
+        const int gam = cp * 32 / GRP;
+        const int prs = kT * (D / 2) + (tau0 * NG + gam) * 4;
+        uint32_t at[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at[i] = sw128_byte(tau0, 2 * (32 * cp + 8 * i), kT);
+        int st = 0, stp = 0, bf = 0, bfp = 0;                  // ring stage and buffer, with their phases
+        for (int j = 0; j < J; ++j) {
+            const uint8_t* stg = sm + C::kOffRing + st * C::kStage;
+            bool f = !mbar_wait_bounded(bar(kBarRing + st), (uint32_t)stp);
+            if (!f && j >= C::kBufs) f = !mbar_wait_bounded(bar(kBarFree + bf), (uint32_t)(bfp ^ 1));
+            uint32_t* bad = reinterpret_cast<uint32_t*>(sm + C::kOffBad) + bf * 80;
+            if (pt < 65) bad[pt] = 0;
+            if (prod_or(f)) { failed = true; break; }
+            uint8_t* buf = sm + bf * C::kBuf;
+            const int64_t inside = w.n - (int64_t)w.k * kT;    // tokens of the tile inside the sequence
+            const int valid = inside < kT ? (int)inside : kT;
+#pragma unroll
+            for (int it = 0; it < 2 * kPer; ++it) {
+                constexpr int kStep = 32;                      // tokens between a thread's items
+                const int side = it / kPer, dt = (it % kPer) * kStep, tau = tau0 + dt;
+                const uint8_t* blk = stg + side * C::kBlockB;
+                const uint4 v = *reinterpret_cast<const uint4*>(blk + src + dt * (D / 2));
+                uint32_t bits = *reinterpret_cast<const uint32_t*>(blk + prs + dt * NG * 4);
+                if (side && tau >= valid) bits = 0u;           // behind the sequence: anything may stand there
+                // rare: a scale of 2^11 or more, a zero of 2^15 or more, infinity or NaN
+                if ((bits & 0x7fffu) >= 0x6800u || (bits & 0x7fff0000u) >= 0x78000000u) {
+                    if (side && ((bits & 0x7c00u) == 0x7c00u || (bits & 0x7c000000u) == 0x7c000000u)) {
+                        bits = 0u;
+                        atomicOr(&bad[tau], 1u << gam);
+                        bad[64] = 1u;
+                    }
+                    // the largest value stays finite in fp16
+                    const __half2 pr = as_h2(bits);
+                    if (fmaf(15.f, __low2float(pr), __high2float(pr)) > 65504.f) bits -= 1u;
+                }
+                const __half2 s2 = __low2half2(as_h2(bits)), z2 = __high2half2(as_h2(bits));
+                const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+                uint8_t* op = buf + side * NL * C::kTile + dt * 128;     // (32 rows further: 4 atoms of 1024 bytes)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t h[4], l[4];
+                    expand_word<NL>(wd[i], s2, z2, h, l);
+                    *reinterpret_cast<uint4*>(op + at[i]) = make_uint4(h[0], h[1], h[2], h[3]);
+                    if constexpr (NL == 2) *reinterpret_cast<uint4*>(op + C::kTile + at[i]) = make_uint4(l[0], l[1], l[2], l[3]);
+                }
+            }
+            fence_proxy_async();
+            mbar_arrive(bar(kBarReady + bf));
+            // every producer is done with the stage before it is filled again
+            prod_or(false);
+            if (pt == 0 && issued < J) {
+                issue(issued);
+                wi.next(a);
+                ++issued;
+            }
+            w.next(a);
+            if (++st == C::kRing) { st = 0; stp ^= 1; }
+            if (++bf == C::kBufs) { bf = 0; bfp ^= 1; }
+        }
+        if (pt == 0) {
+            // copies that may still be in flight (the last one into each stage)
+            for (int j = issued > C::kRing ? issued - C::kRing : 0; j < issued; ++j)
+                mbar_wait_bounded(bar(kBarRing + j % C::kRing), (uint32_t)((j / C::kRing) & 1));
+            if (failed) atomicExch(a.err, 1);
+        }
+    } else if (lane == 0) {
+        // ======================================== the mma thread
+        constexpr uint32_t kIdS = idesc_f16(128, kT), kIdO = idesc_f16_bmn(128, D);
+        W w = w0;
+        bool ok = true;
+        int nP[2] = {0, 0};                // P of each stream waited for so far
+        // S of stream x from buffer bf
+        auto mma_s = [&](int x, int bf) {
+            const uint32_t kb = sbase + (uint32_t)(bf * C::kBuf);
+            const uint32_t xd = tmem + M::kX + 64 * x, qb = tmem + M::kQ + (MT == 2 ? x * QL * (D / 2) : 0);
+            uint32_t acc = 0u;
+#pragma unroll
+            for (int pr = 0; pr < 3; ++pr) {                   // hi hi, lo hi, hi lo
+                if ((pr == 1 && QL == 1) || (pr == 2 && NL == 1)) continue;
+                const uint32_t ql = pr == 1 ? (uint32_t)(D / 2) : 0u, kl = pr == 2 ? (uint32_t)C::kTile : 0u;
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                    tc_mma_f16_ts(xd, qb + ql + 8 * s,
+                                  sw128_desc(kb + kl + (uint32_t)((s >> 2) * (kT * 128) + (s & 3) * 32)), kIdS, acc);
+                    acc = 1u;
+                }
+            }
+            tc_commit(bar(kBarS + x));
+        };
+        // O of stream x (+)= P V from buffer bf, once P is there
+        auto mma_o = [&](int x, int bf, bool first, bool last) -> bool {
+            if (!mbar_wait_bounded(bar(kBarP + x), (uint32_t)(nP[x] & 1))) return false;
+            ++nP[x];
+            tc_fence_after();
+            const uint32_t od = tmem + M::kO + D * x, pa = tmem + M::kX + 64 * x;
+            const uint32_t vb = sbase + (uint32_t)(bf * C::kBuf + NL * C::kTile);
+            uint32_t acc = first ? 0u : 1u;
+#pragma unroll
+            for (int pr = 0; pr < (NL == 2 ? 3 : 1); ++pr) {   // hi hi, lo hi, hi lo
+                const uint32_t pl = pr == 1 ? 32u : 0u, vl = pr == 2 ? (uint32_t)C::kTile : 0u;
+#pragma unroll
+                for (int s = 0; s < kT / 16; ++s) {
+                    tc_mma_f16_ts(od, pa + pl + 8 * s, sw128_desc_mn(vb + vl + 2048 * s, (uint32_t)(kT * 128), 1024u), kIdO,
+                                  acc);
+                    acc = 1u;
+                }
+            }
+            if (last) tc_commit(bar(kBarFree + bf));           // the tile's last product
+            return true;
+        };
+        int seg = 0, jseg = 0;             // segments begun, first tile of this one
+        int pend = -1, pend_buf = 0;       // tile whose O (MT = 2: of stream 1) is still to be issued
+        bool pend_first = false;
+        auto flush = [&]() -> bool {
+            if (pend < 0) return true;
+            const bool r = mma_o(MT == 2 ? 1 : pend & 1, pend_buf, pend_first, true);
+            pend = -1;
+            return r;
+        };
+        int bf = 0, bfp = 0;
+        for (int j = 0; j < J; ++j) {
+            if (j == 0 || w.k == 0) {      // a new unit: its queries replace the last one's
+                if (!(ok = flush())) break;
+                if (j > 0) tc_commit(bar(kBarSeg));
+                if (!(ok = mbar_wait_bounded(bar(kBarQ), (uint32_t)(seg & 1)))) break;
+                ++seg;
+                jseg = j;
+            }
+            if (!(ok = mbar_wait_bounded(bar(kBarReady + bf), (uint32_t)bfp))) break;
+            tc_fence_after();
+            mma_s(MT == 2 ? 0 : j & 1, bf);
+            if (!(ok = flush())) break;    // the other stream's last O
+            if constexpr (MT == 2) {
+                mma_s(1, bf);
+                if (!(ok = mma_o(0, bf, j == jseg, false))) break;
+                pend_first = j == jseg;
+            } else {
+                pend_first = j - jseg < 2;
+            }
+            pend = j;
+            pend_buf = bf;
+            w.next(a);
+            if (++bf == C::kBufs) { bf = 0; bfp ^= 1; }
+        }
+        if (ok) ok = flush();
+        if (ok) tc_commit(bar(kBarSeg));
+        // every mma is done before tensor memory is released
+        tc_commit(bar(kBarDrain));
+        mbar_wait_bounded(bar(kBarDrain), 0u);
+        if (!ok) atomicExch(a.err, 1);
+    }
+    pdl_trigger();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tc_dealloc(tmem, 512);
+    }
+}
+
+template <int D, int GRP, int DT, int MT>
+cudaError_t launch_t(const Int4AttendArgs& a, int num_sms, cudaStream_t s) {
+    using C = Ch<D, GRP, DT == TQ_BF16 ? 1 : 2>;
+    cudaError_t e = set_smem_once<tq_int4_chunk_kernel<D, GRP, DT, MT>>(C::kSmem);
+    if (e != cudaSuccess) return e;
+    const int ctas = num_sms < kInt4MaxCtas ? num_sms : kInt4MaxCtas;
+    if (a.chained) {
+        e = launch_pdl(tq_int4_chunk_kernel<D, GRP, DT, MT>, dim3(ctas), dim3(kThreads), C::kSmem, s, a);
+    } else {
+        tq_int4_chunk_kernel<D, GRP, DT, MT><<<ctas, kThreads, C::kSmem, s>>>(a);
+        e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) return e;
+    return launch_int4_combine<D, DT>(a, 128 * MT, true, ctas, s);
+}
+template <int D, int GRP>
+cudaError_t launch_g(tq_dtype dt, const Int4AttendArgs& a, int num_sms, cudaStream_t s) {
+    const bool two = int4_slot_rows(D, dt, a.rows) == 256;
+    if (dt == TQ_F32) {
+        if constexpr (D == 64)
+            if (two) return launch_t<D, GRP, TQ_F32, 2>(a, num_sms, s);
+        return launch_t<D, GRP, TQ_F32, 1>(a, num_sms, s);
+    }
+    if (dt == TQ_BF16)
+        return two ? launch_t<D, GRP, TQ_BF16, 2>(a, num_sms, s) : launch_t<D, GRP, TQ_BF16, 1>(a, num_sms, s);
+    return two ? launch_t<D, GRP, TQ_F16, 2>(a, num_sms, s) : launch_t<D, GRP, TQ_F16, 1>(a, num_sms, s);
+}
+
+}  // namespace
+
+// 256-row units where there are more than 128 rows and the query limbs leave room for two
+// row tiles in tensor memory (fp32 at head_dim 128: 2 x 128 + 128 + 256 columns do not fit)
+int int4_slot_rows(int d, tq_dtype dt, int rows) {
+    if (d > 128 || rows <= 8) return 8;
+    return rows > 128 && !(d == 128 && dt == TQ_F32) ? 256 : 128;
+}
+
+cudaError_t launch_int4_chunk(int d, int group, tq_dtype dt, const Int4AttendArgs& a, int num_sms, cudaStream_t s) {
+    if (d == 64) return group == 32 ? launch_g<64, 32>(dt, a, num_sms, s) : launch_g<64, 64>(dt, a, num_sms, s);
+    return group == 32   ? launch_g<128, 32>(dt, a, num_sms, s)
+           : group == 64 ? launch_g<128, 64>(dt, a, num_sms, s)
+                         : launch_g<128, 128>(dt, a, num_sms, s);
+}
+
+}  // namespace tqi

@@ -9,7 +9,11 @@ follow (24 2^-23 + 2^-22 < 2^-18.3; half of it on average is under 2^-19, and S
 itself is a bound that signed terms stay far below).  A weight is then off by a
 factor of at most 1 + 2 eps_s relative to the sum, and by the exponential and the
 22-bit limbs (2^-21) and the fp32 sums (at most 2^-19), so an output is off by
-V (2 eps_s + 2^-18), V = the largest |value|, plus half a step of its type."""
+V (2 eps_s + 2^-18), V = the largest |value|, plus half a step of its type.
+
+bf16 calls with more than 8 query rows per kv head round K, V and P to fp16 as
+well (half a step is 2^-11): eps_s grows by 2^-11 S and the output by 2 2^-11 V
+(`rounded`)."""
 import numpy as np
 
 F15 = np.float32(0.06666667014360428)
@@ -74,9 +78,10 @@ def attend(q, k, v, scale, n_q):
     return out
 
 
-def attend_bound(q, kabs, v, scale, out, half_step):
+def attend_bound(q, kabs, v, scale, out, half_step, rounded=False):
     """Largest allowed |error| of the outputs [Lq, d]; kabs [T, d]: |zero| + |scale c|."""
     if len(v) == 0:
         return np.zeros_like(out)
     S = abs(scale) * (np.abs(q) @ kabs.T).max(-1, keepdims=True)
-    return np.abs(v).max() * (2 * S * 2.0 ** -19 + 2.0 ** -18) + half_step * np.abs(out) + 1e-30
+    eps_s = S * (2.0 ** -19 + (2.0 ** -11 if rounded else 0.0))
+    return np.abs(v).max() * (2 * eps_s + 2.0 ** -18 + (2.0 ** -10 if rounded else 0.0)) + half_step * np.abs(out) + 1e-30

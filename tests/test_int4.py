@@ -269,7 +269,7 @@ def run_attend(d, group, dtype, G, Hkv, lens, Lq=1, paged=False, uniform=False, 
                 rows = qn[b, :, hh * G + g]
                 ref = U.attend(rows, k, v, scale, Lq)
                 err = np.abs(got[b, :, hh * G + g] - ref)
-                bound = U.attend_bound(rows, kabs, v, scale, ref, half)
+                bound = U.attend_bound(rows, kabs, v, scale, ref, half, rounded=dtype == "bf16" and Lq * G > 8)
                 if dtype == "f16":
                     bound = bound + 2.0 ** -25        # half a subnormal step
                 assert np.isfinite(got[b, :, hh * G + g]).all()
@@ -299,6 +299,31 @@ def test_attend_lengths(libtq, lens, G, Lq):
 def test_attend_many_rows_and_rows_before_the_first_token(libtq, G, Lq):
     """Row groups of 8, and sequences shorter than the queries: rows that see nothing give zeros."""
     run_attend(128, 64, "bf16", G, 2, [200, 3, 0, 70], Lq=Lq, seed=G)
+
+
+@gpu
+@pytest.mark.parametrize("d,group", [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("G,Lq,lens", [(3, 70, [70, 500, 64, 0, 129]), (1, 9, [9, 1000]), (8, 33, [40, 3]),
+                                       (1, 300, [300, 700])])
+def test_chunks(libtq, d, group, dtype, G, Lq, lens):
+    """Chunks of one and of several row tiles, from the first token on, behind a prefix, and longer than
+    their sequence."""
+    run_attend(d, group, dtype, G, 2, lens, Lq=Lq, paged=(G == 3), seed=G + Lq)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("qmul,vmul,scale", [(1e-6, 1e-4, 1.0), (30.0, 1.0, 1.0), (1.0, 1e3, 0.1), (1.0, 1.0, 0.0),
+                                             (1.0, 1.0, -0.2)])
+def test_chunk_magnitudes(libtq, dtype, qmul, vmul, scale):
+    run_attend(128, 64, dtype, 4, 1, [700, 90], Lq=20, scale=scale, qmul=qmul, vmul=vmul, seed=3)
+
+
+@gpu
+def test_chunk_units_cut_by_many_ctas(libtq):
+    """One kv head and a long cache: every CTA holds a piece of the same row tile."""
+    run_attend(128, 64, "f16", 2, 1, [20000], Lq=10, seed=1)
 
 
 @gpu
