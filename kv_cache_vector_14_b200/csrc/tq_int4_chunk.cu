@@ -3,36 +3,41 @@
 // operand and softmax weights in tensor memory), head_dim 64 and 128, for sm_100a.
 //
 // Mathematics as in tq_int4_attend.cu.  A unit is 128 MT query rows (query i,
-// head g: row i G + g) of one kv head; its tokens come in tiles of 64, one cache
-// block.  A tile is expanded once into shared memory and serves all rows:
-//   S[128 rows][64 tok] = Q K^T      (A: Q in tensor memory, B: K, K-major)
-//   O[128 rows][D]     += P V        (A: P in tensor memory over S, B: V, MN-major)
-// The expanded values zero + scale c are rounded to fp16, bf16 and fp16 queries
-// enter exactly (scaled by a power of two per row), P is fp16.  For bf16 that is
-// one product each (NL = 1): those roundings are 2^-11 relative and the output's
-// own is 2^-8.  For fp16 and fp32 they would show, so K, V and P (and fp32 Q) are
-// kept as fp16 hi + lo (NL = 2, 22 bits) and three products are summed, hi hi +
-// lo hi + hi lo, in the same fp32 accumulator.
+// head g: row i G + g) of one kv head; its tokens come in tiles of TT (128, or 64
+// with two limbs).  A tile is expanded once into shared memory and serves all rows:
+//   S[128 rows][TT] = Q K^T     (A: Q in shared memory, B: K, both K-major)
+//   O[128 rows][D] += P V       (A: P in tensor memory over S, B: V, MN-major)
+// TT = 128 because an mma of N = 64 takes as long as one of N = 128 here (72 clocks
+// measured for either, 64 at the full rate).  The expanded values zero + scale c are
+// rounded to fp16, bf16 and fp16 queries enter exactly (scaled by a power of two per
+// row), P is fp16.  For bf16 that is one product each (NL = 1): those roundings are
+// 2^-11 relative and the output's own is 2^-8.  For fp16 and fp32 they would show, so
+// K, V and P (and fp32 Q) are kept as fp16 hi + lo (NL = 2, 22 bits) and three products
+// are summed, hi hi + lo hi + hi lo, in the same fp32 accumulator.
 //
 // Warp roles: warps 0-3 and 4-7 are two softmax streams, each with its own O
 // accumulator, so that neither waits for the other; a thread owns a row.  With
 // MT = 2 they are the two row tiles of the unit, and an expanded tile serves 256
-// rows; with MT = 1 (few rows, or fp32, whose query limbs leave no tensor memory)
-// they take the even and the odd tiles and are merged at the unit's end.  Warps
-// 8-11 copy blocks (ring of bulk copies) and expand them; warp 12 issues the mma
-// (one thread): while one stream's softmax works, the tensor core runs the other
-// stream's products.  The mma of one thread run in issue order, so a stream's next
-// S cannot overwrite P before its O has read it, and a completed S says that the
-// stream's last O is done, which is when it may be rescaled (the reference
-// exponent moves only when it is exceeded by 2^8).
+// rows; with MT = 1 (few rows, or fp32 at head_dim 128, whose query limbs leave no
+// shared memory) they take the even and the odd tiles and are merged at the unit's
+// end.  Warp 13 fills a ring of cache blocks (bulk copies), warps 8-11 expand them,
+// K and V of a tile in turn; warp 12 issues the mma (one thread): while one stream's
+// softmax works, the tensor core runs the other stream's products.  The mma of one
+// thread run in issue order, so a stream's next S cannot overwrite P before its O
+// has read it, and a completed S says that the stream's last O is done, which is
+// when it may be rescaled (the reference exponent moves only when it is exceeded by
+// 2^8).
 //
 // Work: the units' tiles (each unit only as far as its last row sees) laid end
 // to end, shared out evenly over one CTA per SM on the device, cut units merged
 // by the combine kernel, as in tq_int4_attend.cu.
 //
-// NaN: a value group with a non-finite pair is expanded as zeros and its token
-// marked; rows that see the token get NaN in that group at the end.  So a NaN
-// does not reach the rows for which it is masked, as a product 0 NaN would.
+// NaN: a value group with a non-finite pair is expanded as zeros, and the first
+// such token of the segment is kept per group; rows that see it get NaN in that
+// group at the end (a row sees a prefix of the tokens, so the first one decides).
+// So a NaN does not reach the rows for which it is masked, as a product 0 NaN would.
+#include <climits>
+
 #include "tq_frag.cuh"
 #include "tq_int4.h"
 #include "tq_int4_combine.cuh"
@@ -41,49 +46,49 @@
 namespace tqi {
 namespace {
 
-constexpr int kT = 64;                    // tokens per tile
 constexpr int kSoft = 256;                // softmax threads
 constexpr int kProd = 128;                // producer threads
-constexpr int kThreads = kSoft + kProd + 32;
+constexpr int kThreads = kSoft + kProd + 64;
+constexpr int kSlots = 6;                 // ring of raw cache blocks (64 tokens of K or of V)
 constexpr float kRoom = 7.f, kLazy = 8.f; // P is kept below 2^15 (fp16 holds 65504)
 
-template <int D, int GRP, int NL>
+template <int D, int GRP, int NL, int QL, int MT>
 struct Ch {
     static constexpr int kNG = D / GRP;
+    static constexpr int TT = NL == 1 ? 128 : 64;             // tokens per tile
+    static constexpr int kBlks = TT / 64;                     // cache blocks per tile
     static constexpr int kBlockB = 64 * (D / 2 + 4 * kNG);
-    static constexpr int kTile = kT * D * 2;                  // one fp16 operand of a tile
-    static constexpr int kBuf = 2 * NL * kTile;               // K limbs, V limbs
-    static constexpr int kBufs = NL == 1 ? 3 : 2;
-    static constexpr int kRing = 3;
-    static constexpr int kStage = 2 * kBlockB;
-    static constexpr int kOffRing = kBufs * kBuf;
-    static constexpr int kOffBar = kOffRing + kRing * kStage;
-    static constexpr int kOffBad = kOffBar + 24 * 8;          // per buffer: token marks [64], any mark
-    static constexpr int kOffXch = kOffBad + kBufs * 80 * 4;  // [2][3][128]: reference, sum, NaN groups
-    static constexpr int kOffScan = kOffXch + 6 * 128 * 4;    // [kThreads / 32 + 3] int64
+    static constexpr int kTile = TT * D * 2;                  // one fp16 operand of a tile
+    static constexpr int kQ = 128 * D * 2;                    // one limb of a row tile's queries
+    static constexpr int kBuf = 2 * NL * kTile;               // K limbs, V limbs; two buffers
+    static constexpr int kOffQ = 2 * kBuf;                    // [MT][QL]
+    static constexpr int kOffRing = kOffQ + MT * QL * kQ;
+    static constexpr int kOffBar = kOffRing + kSlots * kBlockB;
+    static constexpr int kOffXch = kOffBar + 32 * 8;          // [2][2][128]: reference, sum
+    static constexpr int kOffBad = kOffXch + 4 * 128 * 4;     // [4 segments][4 groups]: first non-finite token
+    static constexpr int kOffScan = kOffBad + 16 * 4;         // [kThreads / 32 + 3] int64
     static constexpr int kOffMisc = kOffScan + (kThreads / 32 + 3) * 8;
     static constexpr int kSmem = kOffMisc + 16 + 1024;        // + slack to align the base
     static_assert(kOffRing % 16 == 0 && kOffBar % 8 == 0 && kOffScan % 8 == 0, "alignment");
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
-};
-// tensor memory columns
-template <int D, int QL, int MT>
-struct Tm {
-    static constexpr int kQ = 0;                              // MT x QL x D/2
-    static constexpr int kX = MT * QL * D / 2;                // S / P of stream x at kX + 64 x
-    static constexpr int kO = kX + 128;                       // O of stream x at kO + D x
+    // tensor memory columns
+    static constexpr int kX = 0;                              // S / P of stream x at TT x
+    static constexpr int kO = 2 * TT;                         // O of stream x at kO + D x
     static_assert(kO + 2 * D <= 512, "tensor memory");
 };
 
 enum : int {
-    kBarRing = 0,      // [3] raw blocks of a stage in shared memory (copy bytes)
-    kBarReady = 3,     // [3] operands of a buffer built (kProd arrivals)
-    kBarFree = 6,      // [3] operands of a buffer read (commit)
-    kBarS = 9,         // [2] S of stream x computed (commit)
-    kBarP = 11,        // [2] P of stream x written (128 arrivals)
-    kBarSeg = 13,      // O of a segment complete (commit)
-    kBarQ = 14,        // query operand written (256 arrivals)
-    kBarDrain = 15,    // every mma done (commit, at exit)
+    kBarRing = 0,      // [6] a raw block in its slot (copy bytes)
+    kBarSlot = 6,      // [6] a raw block read (kProd arrivals)
+    kBarKReady = 12,   // [2] K operand of a buffer built (kProd arrivals)
+    kBarVReady = 14,   // [2] V operand
+    kBarKFree = 16,    // [2] K operand read (commit)
+    kBarVFree = 18,    // [2] V operand read (commit)
+    kBarS = 20,        // [2] S of stream x computed (commit)
+    kBarP = 22,        // [2] P of stream x written (128 arrivals)
+    kBarSeg = 24,      // O of a segment complete (commit), and the mma thread's own arrival
+    kBarQ = 25,        // query operand written (256 arrivals)
+    kBarDrain = 26,    // every mma done (commit, at exit)
 };
 
 // tokens that the last row of row tile rt sees, and the tiles they take (at least one)
@@ -91,22 +96,22 @@ __device__ __forceinline__ int64_t chunk_len(const Int4AttendArgs& a, int64_t b)
     const int64_t n = (a.lens ? (int64_t)__ldg(a.lens + b) : a.T) + a.add;
     return n < 0 ? 0 : (n > a.Tcap ? a.Tcap : n);
 }
-template <int ROWS>
+template <int ROWS, int TT>
 __device__ __forceinline__ int unit_tiles(const Int4AttendArgs& a, int64_t n, int rt) {
     const int64_t last = (int64_t)rt * ROWS + ROWS - 1 < a.rows ? (int64_t)rt * ROWS + ROWS - 1 : a.rows - 1;
     const int64_t sees = n - a.Lq + 1 + last / a.G;
-    const int64_t t = (sees + kT - 1) / kT;
+    const int64_t t = (sees + TT - 1) / TT;
     return t > 1 ? (int)t : 1;
 }
 
 // Walks the flattened tiles: (sequence, row tile) pair, kv head, tile.
-template <int ROWS>
+template <int ROWS, int TT>
 struct Walk {
     int64_t n;         // tokens of the sequence
     int b, rt, kv, k, nt, R;
     __device__ void load(const Int4AttendArgs& a) {
         n = chunk_len(a, b);
-        nt = unit_tiles<ROWS>(a, n, rt);
+        nt = unit_tiles<ROWS, TT>(a, n, rt);
     }
     __device__ void next(const Int4AttendArgs& a) {
         if (++k < nt) return;
@@ -134,18 +139,6 @@ __device__ __forceinline__ bool soft_or(bool v) {
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
         : "r"((uint32_t)v), "n"(kSoft)
-        : "memory");
-    return r != 0;
-}
-__device__ __forceinline__ bool prod_or(bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 2, %2, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)v), "n"(kProd)
         : "memory");
     return r != 0;
 }
@@ -267,10 +260,9 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
     constexpr int NL = DT == TQ_BF16 ? 1 : 2;                 // limbs of K, V and P
     constexpr int QL = DT == TQ_F32 ? 2 : 1;                  // limbs of Q
     constexpr int ROWS = 128 * MT;
-    using C = Ch<D, GRP, NL>;
-    using M = Tm<D, QL, MT>;
-    using W = Walk<ROWS>;
-    constexpr int NG = C::kNG;
+    using C = Ch<D, GRP, NL, QL, MT>;
+    constexpr int NG = C::kNG, TT = C::TT;
+    using W = Walk<ROWS, TT>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* sm = smem_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -283,20 +275,25 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
     constexpr int kWarps = kThreads / 32;
 
     if (tid == 0) {
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < kSlots; ++i) {
             mbar_init(bar(kBarRing + i), 1);
-            mbar_init(bar(kBarReady + i), kProd);
-            mbar_init(bar(kBarFree + i), 1);
+            mbar_init(bar(kBarSlot + i), kProd);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kBarKReady + i), kProd);
+            mbar_init(bar(kBarVReady + i), kProd);
+            mbar_init(bar(kBarKFree + i), 1);
+            mbar_init(bar(kBarVFree + i), 1);
             mbar_init(bar(kBarS + i), 1);
             mbar_init(bar(kBarP + i), 128);
         }
-        mbar_init(bar(kBarSeg), 1);
+        mbar_init(bar(kBarSeg), 2);
         mbar_init(bar(kBarQ), kSoft);
         mbar_init(bar(kBarDrain), 1);
         fence_mbar_init();
     }
+    int* sBad = reinterpret_cast<int*>(sm + C::kOffBad);
+    if (tid < 16) sBad[tid] = INT_MAX;
     if (warp == 0) {
         tc_alloc(smem_u32(tmem_slot), 512);
         tc_relinquish();
@@ -310,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
     const int64_t p0 = tid * per < pairs ? tid * per : pairs, p1 = p0 + per < pairs ? p0 + per : pairs;
     auto span_of = [&](int64_t p) -> int64_t {
         const int64_t b = p / R;
-        return (int64_t)unit_tiles<ROWS>(a, chunk_len(a, b), (int)(p - b * R)) * a.Hkv;
+        return (int64_t)unit_tiles<ROWS, TT>(a, chunk_len(a, b), (int)(p - b * R)) * a.Hkv;
     };
     int64_t mine = 0;
     for (int64_t p = p0; p < p1; ++p) mine += span_of(p);
@@ -373,9 +370,11 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             const bool rvalid = grow < a.rows;
             const int64_t qi = rvalid ? grow / a.G : 0, qg = rvalid ? grow - qi * a.G : 0;
             const int64_t qrow = ((int64_t)w.b * a.Lq + qi) * a.Hq + (int64_t)w.kv * a.G + qg;
-            const int64_t lim = rvalid ? w.n - a.Lq + 1 + qi : 0;
+            // (a row that is not there sees everything: no masking for it, and nothing of it is stored)
+            const int64_t lim = rvalid ? w.n - a.Lq + 1 + qi : INT64_MAX;
             // query operand: the row scaled by a power of two (largest element in [2^14, 2^15));
-            // with MT = 1 each stream does half of the columns.  Column cc holds positions 2 cc, 2 cc + 1
+            // with MT = 1 each stream does half of the values (position p of a word's eight
+            // holds value word_value(p), as the expanded operands do)
             float fr;
             {
                 constexpr int NQ = MT == 2 ? D : D / 2;
@@ -401,105 +400,122 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 const float f = mx <= 3.4e38f ? exp2f((float)(14 - ex)) : 1.f;
                 const float fs = a.scale_log2 < 0.f ? -f : f;
                 fr = fmaxf(fabsf(a.scale_log2) / f, 1e-37f);  // (above zero: a masked -inf stays one)
-                const uint32_t tq = tl + M::kQ + (MT == 2 ? x * QL * (D / 2) : x * (D / 4));
+                uint8_t* sq = sm + C::kOffQ + (MT == 2 ? x * QL * C::kQ : 0);
 #pragma unroll 1
-                for (int c0 = 0; c0 < NQ / 2; c0 += 16) {
-                    uint32_t qh[16], qlo[16];
+                for (int c0 = 0; c0 < NQ; c0 += 32) {
                     float v[32];
                     if (rvalid) {
-                        load_row<DT, 32>(a.q, qrow * D + q0 + 2 * c0, a.vec16, v);
+                        load_row<DT, 32>(a.q, qrow * D + q0 + c0, a.vec16, v);
                     } else {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) v[e] = 0.f;
                     }
 #pragma unroll
-                    for (int cc = 0; cc < 16; ++cc) {
-                        const int e = 2 * cc & ~7;
-                        split_hilo(v[e + word_value(2 * cc & 7)] * fs, v[e + word_value((2 * cc & 7) + 1)] * fs, qh[cc], qlo[cc]);
+                    for (int i = 0; i < 32; i += 8) {          // eight positions, 16 bytes
+                        uint32_t qh[4], qlo[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            split_hilo(v[i + word_value(2 * k)] * fs, v[i + word_value(2 * k + 1)] * fs, qh[k], qlo[k]);
+                        const uint32_t at = sw128_byte(r, 2 * (q0 + c0 + i), 128);
+                        *reinterpret_cast<uint4*>(sq + at) = make_uint4(qh[0], qh[1], qh[2], qh[3]);
+                        if constexpr (QL == 2)
+                            *reinterpret_cast<uint4*>(sq + C::kQ + at) = make_uint4(qlo[0], qlo[1], qlo[2], qlo[3]);
                     }
-                    tc_st16(tq + c0, qh);
-                    if constexpr (QL == 2) tc_st16(tq + D / 2 + c0, qlo);
                 }
-                tc_wait_st();
-                tc_fence_before();
+                fence_proxy_async();
                 mbar_arrive(bar(kBarQ));
             }
             float mref = -INFINITY, lsum = 0.f;
-            uint32_t nanmask = 0;
             bool any = false;                                  // this stream has an O
-            const uint32_t tx = tl + M::kX + 64 * x;
+            const uint32_t tx = tl + C::kX + TT * x;
             const uint64_t fr2 = pack2(fr, fr);
             for (int jj = MT == 2 ? j : j + ((j & 1) ^ x); jj < j1 && !failed; jj += 3 - MT) {
-                const int k = k0 + (jj - j);
+                const int64_t tok0 = (int64_t)(k0 + (jj - j)) * TT;
                 if (!warp_wait(bar(kBarS + x), (uint32_t)(nS & 1))) { failed = true; break; }
                 ++nS;
                 tc_fence_after();
-                uint32_t sv[64];
-                tc_ld64(tx, sv);
-                const int64_t tok0 = (int64_t)k * kT;
-                const int vis = lim - tok0 >= kT ? kT : (int)(lim > tok0 ? lim - tok0 : 0);
-                if (vis < kT) {
-#pragma unroll
-                    for (int t = 0; t < kT; ++t)
-                        if (t >= vis) sv[t] = 0xff800000u;
-                }
-                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int t = 0; t < kT; t += 8)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        mx4[q] = fmaxf(mx4[q], fmaxf(__uint_as_float(sv[t + 2 * q]), __uint_as_float(sv[t + 2 * q + 1])));
-                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fr;
-                // move the reference when it is exceeded by 2^kLazy; O is rescaled by whole warps
-                const bool move = mx - kRoom - kLazy > mref;
-                if (__any_sync(kFull, move)) {
-                    float f = 1.f;
-                    if (move) {
-                        f = mref == -INFINITY ? 0.f : fast_exp2(mref - (mx - kRoom));
-                        mref = mx - kRoom;
-                        lsum *= f;
-                    }
-                    if (any) {
+                // 64 tokens at a time; P of tokens 2 i, 2 i + 1 goes to column i, over scores that
+                // have been read (NL = 2: low limbs to column 32 + i)
 #pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 16) {
-                            uint32_t ov[16];
-                            tc_ld16(tl + M::kO + D * x + c0, ov);
+                for (int h = 0; h < TT / 64; ++h) {
+                    uint32_t sv[64];
+                    tc_ld64(tx + 64 * h, sv);
+                    const int64_t rest = lim - tok0 - 64 * h;
+                    const int vis = rest >= 64 ? 64 : (int)(rest > 0 ? rest : 0);
+                    if (vis < 64) {
 #pragma unroll
-                            for (int cc = 0; cc < 16; ++cc) ov[cc] = __float_as_uint(__uint_as_float(ov[cc]) * f);
-                            tc_st16(tl + M::kO + D * x + c0, ov);
-                        }
+                        for (int t = 0; t < 64; ++t)
+                            if (t >= vis) sv[t] = 0xff800000u;
                     }
+                    // P = 2^(S fr - mref) and its sum; 16 tokens at a time (fewer registers)
+                    float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    auto weights = [&](float m) -> float {
+                        const uint64_t m2 = pack2(-m, -m);
+                        uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+                        for (int qt = 0; qt < 4; ++qt) {
+                            uint32_t ph[8], pl[8];
+#pragma unroll
+                            for (int t = 0; t < 16; t += 2) {
+                                const float a0 = __uint_as_float(sv[16 * qt + t]), a1 = __uint_as_float(sv[16 * qt + t + 1]);
+                                mx4[(t >> 1) & 3] = fmaxf(mx4[(t >> 1) & 3], fmaxf(a0, a1));
+                                float e0, e1;
+                                unpack2(fma2(pack2(a0, a1), fr2, m2), e0, e1);
+                                e0 = fast_exp2(e0);
+                                e1 = fast_exp2(e1);
+                                sum2[(t >> 1) & 1] = add2(sum2[(t >> 1) & 1], pack2(e0, e1));
+                                if constexpr (NL == 2) split_hilo(e0, e1, ph[t >> 1], pl[t >> 1]);
+                                else ph[t >> 1] = h2_bits(__floats2half2_rn(e0, e1));
+                            }
+                            tc_st8(tx + 32 * h + 8 * qt, ph);
+                            if constexpr (NL == 2) tc_st8(tx + 32 + 8 * qt, pl);
+                        }
+                        float s0, s1;
+                        unpack2(add2(sum2[0], sum2[1]), s0, s1);
+                        return s0 + s1;
+                    };
+                    // The weights are taken with the reference as it is, the maximum beside them (off the
+                    // critical path); where the reference turns out exceeded by 2^kLazy (always in a unit's
+                    // first tile) it moves, O and the tile's earlier weights are rescaled by whole warps, and
+                    // the weights are taken again.
+                    float sum = weights(mref == -INFINITY ? 0.f : mref);
+                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fr;
+                    const bool move = mx - kRoom - kLazy > mref;
+                    if (__any_sync(kFull, move)) {
+                        float f = 1.f;
+                        if (move) {
+                            f = mref == -INFINITY ? 0.f : fast_exp2(mref - (mx - kRoom));
+                            mref = mx - kRoom;
+                            lsum *= f;
+                        }
+                        if (any) {
+#pragma unroll 1
+                            for (int c0 = 0; c0 < D; c0 += 16) {
+                                uint32_t ov[16];
+                                tc_ld16(tl + C::kO + D * x + c0, ov);
+#pragma unroll
+                                for (int cc = 0; cc < 16; ++cc) ov[cc] = __float_as_uint(__uint_as_float(ov[cc]) * f);
+                                tc_st16(tl + C::kO + D * x + c0, ov);
+                            }
+                        }
+                        if (h > 0) {
+                            tc_wait_st();
+                            const __half2 f2 = __float2half2_rn(f);
+#pragma unroll 1
+                            for (int c0 = 0; c0 < 32 * h; c0 += 16) {
+                                uint32_t pv[16];
+                                tc_ld16(tx + c0, pv);
+#pragma unroll
+                                for (int cc = 0; cc < 16; ++cc) pv[cc] = f == 0.f ? 0u : h2_bits(__hmul2(as_h2(pv[cc]), f2));
+                                tc_st16(tx + c0, pv);
+                            }
+                        }
+                        sum = weights(mref == -INFINITY ? 0.f : mref);
+                    }
+                    lsum += sum;
                 }
                 any = true;
-                const float m = mref == -INFINITY ? 0.f : mref;
-                const uint64_t m2 = pack2(-m, -m);
-                uint64_t sum2[2] = {0ull, 0ull};
-#pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {               // 32 tokens at a time: fewer registers
-                    uint32_t ph[16], pl[16];
-#pragma unroll
-                    for (int t = 0; t < 32; t += 2) {
-                        float e0, e1;
-                        unpack2(fma2(pack2(__uint_as_float(sv[32 * hf + t]), __uint_as_float(sv[32 * hf + t + 1])), fr2, m2),
-                                e0, e1);
-                        e0 = fast_exp2(e0);
-                        e1 = fast_exp2(e1);
-                        sum2[(t >> 1) & 1] = add2(sum2[(t >> 1) & 1], pack2(e0, e1));
-                        if constexpr (NL == 2) split_hilo(e0, e1, ph[t >> 1], pl[t >> 1]);
-                        else ph[t >> 1] = h2_bits(__floats2half2_rn(e0, e1));
-                    }
-                    tc_st16(tx + 16 * hf, ph);
-                    if constexpr (NL == 2) tc_st16(tx + 32 + 16 * hf, pl);
-                }
-                float s0, s1;
-                unpack2(add2(sum2[0], sum2[1]), s0, s1);
-                lsum += s0 + s1;
                 tc_wait_st();
-                // tokens marked by the producers
-                const uint32_t* bad = reinterpret_cast<const uint32_t*>(sm + C::kOffBad) + (jj % C::kBufs) * 80;
-                if (!warp_wait(bar(kBarReady + jj % C::kBufs), (uint32_t)((jj / C::kBufs) & 1))) { failed = true; break; }
-                if (bad[64])
-                    for (int t = 0; t < vis; ++t) nanmask |= bad[t];
                 tc_fence_before();
                 mbar_arrive(bar(kBarP + x));
             }
@@ -508,21 +524,22 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             tc_fence_after();
             if (!any) mref = -INFINITY;
             if (lsum != lsum && mref == -INFINITY) mref = 0.f;   // nothing but NaN scores
-            xch[(x * 3 + 0) * 128 + r] = mref;
-            xch[(x * 3 + 1) * 128 + r] = lsum;
-            xch[(x * 3 + 2) * 128 + r] = __uint_as_float(nanmask);
+            // groups with a non-finite pair on a token that this row sees
+            uint32_t bad = 0;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) bad |= (uint32_t)((int64_t)sBad[4 * (seg & 3) + g] < lim) << g;
+            xch[x * 128 + r] = mref;
+            xch[(2 + x) * 128 + r] = lsum;
             if (soft_or(failed)) failed = true;
             const bool begins = k0 == 0, ends = j1 - j == left, whole = begins && ends;
             const int64_t slot = (2 * c + (begins ? 1 : 0)) * ROWS + ur;
             // MT = 1: both streams' results, each stream half of the coordinates
             float m0 = mref, m1 = -INFINITY, l0 = lsum, l1 = 0.f;
-            uint32_t bad = nanmask;
             if constexpr (MT == 1) {
                 m0 = xch[r];
-                m1 = xch[3 * 128 + r];
-                l0 = xch[128 + r];
-                l1 = xch[4 * 128 + r];
-                bad = __float_as_uint(xch[2 * 128 + r]) | __float_as_uint(xch[5 * 128 + r]);
+                m1 = xch[128 + r];
+                l0 = xch[2 * 128 + r];
+                l1 = xch[3 * 128 + r];
             }
             const float mm = failed ? -INFINITY : fmaxf(m0, m1);
             const float f0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - mm), f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - mm);
@@ -533,8 +550,8 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             for (int c0 = 0; c0 < kCols; c0 += 32) {
                 const int col = MT == 2 ? c0 : x * (D / 2) + c0;
                 uint32_t o0[32], o1[32];
-                tc_ld32(tl + M::kO + (MT == 2 ? D * x : 0) + col, o0);
-                if constexpr (MT == 1) tc_ld32(tl + M::kO + D + col, o1);
+                tc_ld32(tl + C::kO + (MT == 2 ? D * x : 0) + col, o0);
+                if constexpr (MT == 1) tc_ld32(tl + C::kO + D + col, o1);
                 const bool poison = (bad >> (col / GRP)) & 1u; // (a run of 32 lies in one group)
                 if (!rvalid) continue;
                 float v[32];
@@ -565,7 +582,9 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 const int64_t end = lo + j + left;             // (flattened index behind its last tile)
                 a.split[c] = make_int4(w.b, w.rt * (int)a.Hkv + w.kv, (int)((end * nC - 1) / N), 1);
             }
-            // the next segment's queries and exchange overwrite what was read here
+            // the next segment's queries and exchange overwrite what was read here (the marks of
+            // this segment's slot are next used four segments on; producers are at most two ahead)
+            if (tid < 4) sBad[4 * (seg & 3) + tid] = INT_MAX;
             tc_fence_before();
             soft_or(false);
             tc_fence_after();
@@ -575,178 +594,208 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
         }
         if (failed) atomicExch(a.err, 1);
     } else if (warp < 12) {
-        // ======================================== producers: thread = token `tau` (and tau + 32)
-        // of piece cp (32 values; D = 64: two warps share a piece), K and V
-        const int pt = tid - kSoft;
-        W wi = w0, w = w0;
-        auto issue = [&](int j) {
-            uint8_t* stg = sm + C::kOffRing + (j % C::kRing) * C::kStage;
-            const uint32_t br = bar(kBarRing + j % C::kRing);
-            const int64_t bh = (int64_t)wi.b * a.Hkv + wi.kv;
-            const bool some = wi.n > 0;
-            const int64_t kb = some ? cache_block(a.ktable, a.kpool, a.NB, bh, wi.k, a.err) : 0;
-            const int64_t vb = some ? cache_block(a.vtable, a.vpool, a.NB, bh, wi.k, a.err) : 0;
-            mbar_expect_tx(br, (uint32_t)C::kStage);
-            bulk_g2s(smem_u32(stg), a.kc + (kb >= 0 ? kb : 0) * C::kBlockB, C::kBlockB, br);
-            bulk_g2s(smem_u32(stg + C::kBlockB), a.vc + (vb >= 0 ? vb : 0) * C::kBlockB, C::kBlockB, br);
-        };
-        int issued = 0;
-        if (pt == 0) {
-            asm volatile("fence.proxy.async;" ::: "memory");
-            for (; issued < C::kRing && issued < J; ++issued) {
-                issue(issued);
-                wi.next(a);
-            }
-        }
-        constexpr int kPieces = D / 32, kPer = kT * kPieces / kProd;     // items per side and thread
-        const int cp = (pt >> 5) % kPieces, tau0 = lane + 32 * ((pt >> 5) / kPieces);
+        // ======================================== producers: thread = token `tau0` (D = 128: and
+        // tau0 + 32) of piece cp (32 values) of a block
+        const int pw = warp - 8;
+        W w = w0;
+        constexpr int kPieces = D / 32, kItems = 64 * kPieces / kProd;   // items per block and thread
+        const int cp = pw % kPieces, tau0 = lane + 32 * (pw / kPieces);
         const int src = tau0 * (D / 2) + ((cp * 16) ^ int4_swizzle(D, tau0));
         const int gam = cp * 32 / GRP;
-        const int prs = kT * (D / 2) + (tau0 * NG + gam) * 4;
+        const int prs = 64 * (D / 2) + (tau0 * NG + gam) * 4;
         uint32_t at[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) at[i] = sw128_byte(tau0, 2 * (32 * cp + 8 * i), kT);
-        int st = 0, stp = 0, bf = 0, bfp = 0;                  // ring stage and buffer, with their phases
-        for (int j = 0; j < J; ++j) {
-            const uint8_t* stg = sm + C::kOffRing + st * C::kStage;
-            bool f = !mbar_wait_bounded(bar(kBarRing + st), (uint32_t)stp);
-            if (!f && j >= C::kBufs) f = !mbar_wait_bounded(bar(kBarFree + bf), (uint32_t)(bfp ^ 1));
-            uint32_t* bad = reinterpret_cast<uint32_t*>(sm + C::kOffBad) + bf * 80;
-            if (pt < 65) bad[pt] = 0;
-            if (prod_or(f)) { failed = true; break; }
-            uint8_t* buf = sm + bf * C::kBuf;
-            const int64_t inside = w.n - (int64_t)w.k * kT;    // tokens of the tile inside the sequence
-            const int valid = inside < kT ? (int)inside : kT;
+        for (int i = 0; i < 4; ++i) at[i] = sw128_byte(tau0, 2 * (32 * cp + 8 * i), TT);
+        int slot = 0, sp = 0, bf = 0, bfp = 0, seg = 0;        // ring slot and buffer, with their phases
+        for (int j = 0; j < J && !failed; ++j) {
+#pragma unroll 1
+            for (int side = 0; side < 2 && !failed; ++side) {  // K, then V
+                if (j >= 2 && !warp_wait(bar((side ? kBarVFree : kBarKFree) + bf), (uint32_t)(bfp ^ 1))) { failed = true; break; }
+#pragma unroll 1
+                for (int blk = 0; blk < C::kBlks; ++blk) {
+                    if (!warp_wait(bar(kBarRing + slot), (uint32_t)sp)) { failed = true; break; }
+                    const uint8_t* raw_blk = sm + C::kOffRing + slot * C::kBlockB;
+                    const int64_t tok0 = (int64_t)w.k * TT + 64 * blk, inside = w.n - tok0;
+                    const int valid = inside < 64 ? (int)(inside > 0 ? inside : 0) : 64;   // tokens inside the sequence
+                    uint4 v[kItems];
+                    uint32_t bits[kItems];
+                    bool rare = false;
 #pragma unroll
-            for (int it = 0; it < 2 * kPer; ++it) {
-                constexpr int kStep = 32;                      // tokens between a thread's items
-                const int side = it / kPer, dt = (it % kPer) * kStep, tau = tau0 + dt;
-                const uint8_t* blk = stg + side * C::kBlockB;
-                const uint4 v = *reinterpret_cast<const uint4*>(blk + src + dt * (D / 2));
-                uint32_t bits = *reinterpret_cast<const uint32_t*>(blk + prs + dt * NG * 4);
-                if (side && tau >= valid) bits = 0u;           // behind the sequence: anything may stand there
-                // rare: a scale of 2^11 or more, a zero of 2^15 or more, infinity or NaN
-                if ((bits & 0x7fffu) >= 0x6800u || (bits & 0x7fff0000u) >= 0x78000000u) {
-                    if (side && ((bits & 0x7c00u) == 0x7c00u || (bits & 0x7c000000u) == 0x7c000000u)) {
-                        bits = 0u;
-                        atomicOr(&bad[tau], 1u << gam);
-                        bad[64] = 1u;
+                    for (int it = 0; it < kItems; ++it) {
+                        v[it] = *reinterpret_cast<const uint4*>(raw_blk + src + 32 * it * (D / 2));
+                        bits[it] = *reinterpret_cast<const uint32_t*>(raw_blk + prs + 32 * it * NG * 4);
+                        // behind the sequence anything may stand
+                        if (tau0 + 32 * it >= valid) bits[it] = 0u;
+                        // a scale of 2^11 or more, a zero of 2^15 or more, infinity or NaN
+                        rare |= (bits[it] & 0x7fffu) >= 0x6800u || (bits[it] & 0x7fff0000u) >= 0x78000000u;
                     }
-                    // the largest value stays finite in fp16
-                    const __half2 pr = as_h2(bits);
-                    if (fmaf(15.f, __low2float(pr), __high2float(pr)) > 65504.f) bits -= 1u;
-                }
-                const __half2 s2 = __low2half2(as_h2(bits)), z2 = __high2half2(as_h2(bits));
-                const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
-                uint8_t* op = buf + side * NL * C::kTile + dt * 128;     // (32 rows further: 4 atoms of 1024 bytes)
+                    if (rare) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t h[4], l[4];
-                    expand_word<NL>(wd[i], s2, z2, h, l);
-                    *reinterpret_cast<uint4*>(op + at[i]) = make_uint4(h[0], h[1], h[2], h[3]);
-                    if constexpr (NL == 2) *reinterpret_cast<uint4*>(op + C::kTile + at[i]) = make_uint4(l[0], l[1], l[2], l[3]);
+                        for (int it = 0; it < kItems; ++it) {
+                            if (side && ((bits[it] & 0x7c00u) == 0x7c00u || (bits[it] & 0x7c000000u) == 0x7c000000u)) {
+                                bits[it] = 0u;
+                                atomicMin(&sBad[4 * (seg & 3) + gam], (int)tok0 + tau0 + 32 * it);
+                            }
+                            // the largest value stays finite in fp16
+                            if (fmaf(15.f, __low2float(as_h2(bits[it])), __high2float(as_h2(bits[it]))) > 65504.f) bits[it] -= 1u;
+                        }
+                    }
+                    uint8_t* buf = sm + bf * C::kBuf + side * NL * C::kTile + blk * 64 * 128;
+#pragma unroll
+                    for (int it = 0; it < kItems; ++it) {
+                        const __half2 s2 = __low2half2(as_h2(bits[it])), z2 = __high2half2(as_h2(bits[it]));
+                        const uint32_t wd[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
+                        uint8_t* op = buf + 32 * it * 128;     // (32 rows further: 4 atoms of 1024 bytes)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t h[4], l[4];
+                            expand_word<NL>(wd[i], s2, z2, h, l);
+                            *reinterpret_cast<uint4*>(op + at[i]) = make_uint4(h[0], h[1], h[2], h[3]);
+                            if constexpr (NL == 2)
+                                *reinterpret_cast<uint4*>(op + C::kTile + at[i]) = make_uint4(l[0], l[1], l[2], l[3]);
+                        }
+                    }
+                    fence_proxy_async();   // operands for the tensor core; the slot's reads before its next copy
+                    mbar_arrive(bar(kBarSlot + slot));
+                    if (++slot == kSlots) { slot = 0; sp ^= 1; }
                 }
+                if (!failed) mbar_arrive(bar((side ? kBarVReady : kBarKReady) + bf));
             }
-            fence_proxy_async();
-            mbar_arrive(bar(kBarReady + bf));
-            // every producer is done with the stage before it is filled again
-            prod_or(false);
-            if (pt == 0 && issued < J) {
-                issue(issued);
-                wi.next(a);
-                ++issued;
-            }
+            if ((bf ^= 1) == 0) bfp ^= 1;
+            if (w.k == w.nt - 1) ++seg;
             w.next(a);
-            if (++st == C::kRing) { st = 0; stp ^= 1; }
-            if (++bf == C::kBufs) { bf = 0; bfp ^= 1; }
         }
-        if (pt == 0) {
-            // copies that may still be in flight (the last one into each stage)
-            for (int j = issued > C::kRing ? issued - C::kRing : 0; j < issued; ++j)
-                mbar_wait_bounded(bar(kBarRing + j % C::kRing), (uint32_t)((j / C::kRing) & 1));
+        if (failed && lane == 0) atomicExch(a.err, 1);
+    } else if (warp == 13) {
+        // ======================================== loader: one thread fills the ring, per tile the K
+        // blocks and then the V blocks
+        if (lane == 0) {
+            W w = w0;
+            int i = 0, slot = 0, sp = 0;                       // blocks loaded
+            asm volatile("fence.proxy.async;" ::: "memory");
+            for (int j = 0; j < J && !failed; ++j) {
+                const int64_t bh = (int64_t)w.b * a.Hkv + w.kv;
+                int64_t blk[2 * C::kBlks];
+#pragma unroll
+                for (int k = 0; k < 2 * C::kBlks; ++k) {
+                    // (a tile may reach behind the last block: that one again, its tokens count as absent)
+                    const int64_t last = w.n > 0 ? (w.n - 1) >> 6 : 0, lb = (int64_t)w.k * C::kBlks + k % C::kBlks;
+                    const bool v = k >= C::kBlks;
+                    const int64_t p = w.n > 0 ? cache_block(v ? a.vtable : a.ktable, v ? a.vpool : a.kpool, a.NB, bh,
+                                                            lb < last ? lb : last, a.err)
+                                              : 0;
+                    blk[k] = p >= 0 ? p : 0;                   // a bad table entry reads block 0
+                }
+#pragma unroll
+                for (int k = 0; k < 2 * C::kBlks; ++k) {
+                    if (i >= kSlots && !mbar_wait_bounded(bar(kBarSlot + slot), (uint32_t)(sp ^ 1))) { failed = true; break; }
+                    const uint32_t br = bar(kBarRing + slot);
+                    mbar_expect_tx(br, (uint32_t)C::kBlockB);
+                    bulk_g2s(smem_u32(sm + C::kOffRing + slot * C::kBlockB),
+                             (k >= C::kBlks ? a.vc : a.kc) + blk[k] * C::kBlockB, C::kBlockB, br);
+                    ++i;
+                    if (++slot == kSlots) { slot = 0; sp ^= 1; }
+                }
+                w.next(a);
+            }
+            // copies that may still be in flight (the last one into each slot)
+            for (int k = i > kSlots ? i - kSlots : 0; k < i; ++k)
+                mbar_wait_bounded(bar(kBarRing + k % kSlots), (uint32_t)((k / kSlots) & 1));
             if (failed) atomicExch(a.err, 1);
         }
     } else if (lane == 0) {
         // ======================================== the mma thread
-        constexpr uint32_t kIdS = idesc_f16(128, kT), kIdO = idesc_f16_bmn(128, D);
+        constexpr uint32_t kIdS = idesc_f16(128, TT), kIdO = idesc_f16_bmn(128, D);
         W w = w0;
         bool ok = true;
+        // operand descriptors of buffer 0; an offset goes into their address field (16-byte units;
+        // shared-memory addresses are below 2^18, so it does not carry)
+        const uint64_t qdesc = sw128_desc(sbase + C::kOffQ), kdesc = sw128_desc(sbase);
+        const uint64_t vdesc = sw128_desc_mn(sbase + NL * C::kTile, (uint32_t)(TT * 128), 1024u);
         int nP[2] = {0, 0};                // P of each stream waited for so far
         // S of stream x from buffer bf
-        auto mma_s = [&](int x, int bf) {
-            const uint32_t kb = sbase + (uint32_t)(bf * C::kBuf);
-            const uint32_t xd = tmem + M::kX + 64 * x, qb = tmem + M::kQ + (MT == 2 ? x * QL * (D / 2) : 0);
+        auto mma_s = [&](int x, int bf, bool last) {
+            const uint64_t kd = kdesc + (uint64_t)(bf * (C::kBuf >> 4));
+            const uint64_t qd = qdesc + (uint64_t)(MT == 2 ? x * ((QL * C::kQ) >> 4) : 0);
+            const uint32_t xd = tmem + C::kX + TT * x;
             uint32_t acc = 0u;
 #pragma unroll
             for (int pr = 0; pr < 3; ++pr) {                   // hi hi, lo hi, hi lo
                 if ((pr == 1 && QL == 1) || (pr == 2 && NL == 1)) continue;
-                const uint32_t ql = pr == 1 ? (uint32_t)(D / 2) : 0u, kl = pr == 2 ? (uint32_t)C::kTile : 0u;
+                const uint32_t ql = pr == 1 ? (uint32_t)C::kQ : 0u, kl = pr == 2 ? (uint32_t)C::kTile : 0u;
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
-                    tc_mma_f16_ts(xd, qb + ql + 8 * s,
-                                  sw128_desc(kb + kl + (uint32_t)((s >> 2) * (kT * 128) + (s & 3) * 32)), kIdS, acc);
+                    tc_mma_f16_ss(xd, qd + ((ql + (uint32_t)((s >> 2) * (128 * 128) + (s & 3) * 32)) >> 4),
+                                  kd + ((kl + (uint32_t)((s >> 2) * (TT * 128) + (s & 3) * 32)) >> 4), kIdS, acc);
                     acc = 1u;
                 }
             }
             tc_commit(bar(kBarS + x));
+            if (last) tc_commit(bar(kBarKFree + bf));          // the tile's last use of K
         };
-        // O of stream x (+)= P V from buffer bf, once P is there
-        auto mma_o = [&](int x, int bf, bool first, bool last) -> bool {
+        // O of stream x (+)= P V from buffer bf, once P (and V) are there
+        auto mma_o = [&](int x, int bf, uint32_t vphase, bool first, bool last) -> bool {
+            if (!mbar_wait_bounded(bar(kBarVReady + bf), vphase)) return false;
             if (!mbar_wait_bounded(bar(kBarP + x), (uint32_t)(nP[x] & 1))) return false;
             ++nP[x];
             tc_fence_after();
-            const uint32_t od = tmem + M::kO + D * x, pa = tmem + M::kX + 64 * x;
-            const uint32_t vb = sbase + (uint32_t)(bf * C::kBuf + NL * C::kTile);
+            const uint32_t od = tmem + C::kO + D * x, pa = tmem + C::kX + TT * x;
+            const uint64_t vd = vdesc + (uint64_t)(bf * (C::kBuf >> 4));
             uint32_t acc = first ? 0u : 1u;
 #pragma unroll
             for (int pr = 0; pr < (NL == 2 ? 3 : 1); ++pr) {   // hi hi, lo hi, hi lo
                 const uint32_t pl = pr == 1 ? 32u : 0u, vl = pr == 2 ? (uint32_t)C::kTile : 0u;
 #pragma unroll
-                for (int s = 0; s < kT / 16; ++s) {
-                    tc_mma_f16_ts(od, pa + pl + 8 * s, sw128_desc_mn(vb + vl + 2048 * s, (uint32_t)(kT * 128), 1024u), kIdO,
-                                  acc);
+                for (int s = 0; s < TT / 16; ++s) {
+                    tc_mma_f16_ts(od, pa + pl + 8 * s, vd + ((vl + 2048 * s) >> 4), kIdO, acc);
                     acc = 1u;
                 }
             }
-            if (last) tc_commit(bar(kBarFree + bf));           // the tile's last product
+            if (last) tc_commit(bar(kBarVFree + bf));          // the tile's last use of V
             return true;
         };
         int seg = 0, jseg = 0;             // segments begun, first tile of this one
         int pend = -1, pend_buf = 0;       // tile whose O (MT = 2: of stream 1) is still to be issued
+        uint32_t pend_phase = 0;
         bool pend_first = false;
         auto flush = [&]() -> bool {
             if (pend < 0) return true;
-            const bool r = mma_o(MT == 2 ? 1 : pend & 1, pend_buf, pend_first, true);
+            const bool r = mma_o(MT == 2 ? 1 : pend & 1, pend_buf, pend_phase, pend_first, true);
             pend = -1;
             return r;
+        };
+        auto segment_done = [&]() {
+            tc_commit(bar(kBarSeg));
+            mbar_arrive(bar(kBarSeg));     // (orders what the producers noted, seen through their arrivals)
         };
         int bf = 0, bfp = 0;
         for (int j = 0; j < J; ++j) {
             if (j == 0 || w.k == 0) {      // a new unit: its queries replace the last one's
                 if (!(ok = flush())) break;
-                if (j > 0) tc_commit(bar(kBarSeg));
+                if (j > 0) segment_done();
                 if (!(ok = mbar_wait_bounded(bar(kBarQ), (uint32_t)(seg & 1)))) break;
                 ++seg;
                 jseg = j;
             }
-            if (!(ok = mbar_wait_bounded(bar(kBarReady + bf), (uint32_t)bfp))) break;
+            if (!(ok = mbar_wait_bounded(bar(kBarKReady + bf), (uint32_t)bfp))) break;
             tc_fence_after();
-            mma_s(MT == 2 ? 0 : j & 1, bf);
+            mma_s(MT == 2 ? 0 : j & 1, bf, MT == 1);
             if (!(ok = flush())) break;    // the other stream's last O
             if constexpr (MT == 2) {
-                mma_s(1, bf);
-                if (!(ok = mma_o(0, bf, j == jseg, false))) break;
+                mma_s(1, bf, true);
+                if (!(ok = mma_o(0, bf, (uint32_t)bfp, j == jseg, false))) break;
                 pend_first = j == jseg;
             } else {
                 pend_first = j - jseg < 2;
             }
             pend = j;
             pend_buf = bf;
+            pend_phase = (uint32_t)bfp;
             w.next(a);
-            if (++bf == C::kBufs) { bf = 0; bfp ^= 1; }
+            if ((bf ^= 1) == 0) bfp ^= 1;
         }
         if (ok) ok = flush();
-        if (ok) tc_commit(bar(kBarSeg));
+        if (ok) segment_done();
         // every mma is done before tensor memory is released
         tc_commit(bar(kBarDrain));
         mbar_wait_bounded(bar(kBarDrain), 0u);
@@ -763,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
 
 template <int D, int GRP, int DT, int MT>
 cudaError_t launch_t(const Int4AttendArgs& a, int num_sms, cudaStream_t s) {
-    using C = Ch<D, GRP, DT == TQ_BF16 ? 1 : 2>;
+    using C = Ch<D, GRP, DT == TQ_BF16 ? 1 : 2, DT == TQ_F32 ? 2 : 1, MT>;
     cudaError_t e = set_smem_once<tq_int4_chunk_kernel<D, GRP, DT, MT>>(C::kSmem);
     if (e != cudaSuccess) return e;
     const int ctas = num_sms < kInt4MaxCtas ? num_sms : kInt4MaxCtas;
@@ -791,8 +840,8 @@ cudaError_t launch_g(tq_dtype dt, const Int4AttendArgs& a, int num_sms, cudaStre
 
 }  // namespace
 
-// 256-row units where there are more than 128 rows and the query limbs leave room for two
-// row tiles in tensor memory (fp32 at head_dim 128: 2 x 128 + 128 + 256 columns do not fit)
+// 256-row units where there are more than 128 rows and two row tiles' query limbs fit into
+// shared memory (fp32 at head_dim 128: 128 KB of them beside 128 KB of operands do not)
 int int4_slot_rows(int d, tq_dtype dt, int rows) {
     if (d > 128 || rows <= 8) return 8;
     return rows > 128 && !(d == 128 && dt == TQ_F32) ? 256 : 128;
