@@ -3,30 +3,28 @@
 // operand and softmax weights in tensor memory), head_dim 64 and 128, for sm_100a.
 //
 // Mathematics as in tq_int4_attend.cu.  A unit is 128 MT query rows (query i,
-// head g: row i G + g) of one kv head; its tokens come in tiles of TT (128, or 64
-// with two limbs).  A tile is expanded once into shared memory and serves all rows:
-//   S[128 rows][TT] = Q K^T     (A: Q in shared memory, B: K, both K-major)
+// head g: row i G + g) of one kv head; its tokens come in tiles of 64, one cache
+// block.  A tile is expanded once into shared memory and serves all rows:
+//   S[128 rows][64] = Q K^T     (A: Q in shared memory, B: K, both K-major)
 //   O[128 rows][D] += P V       (A: P in tensor memory over S, B: V, MN-major)
-// TT = 128 because an mma of N = 64 takes as long as one of N = 128 here (72 clocks
-// measured for either, 64 at the full rate).  The expanded values zero + scale c are
-// rounded to fp16, bf16 and fp16 queries enter exactly (scaled by a power of two per
-// row), P is fp16.  For bf16 that is one product each (NL = 1): those roundings are
-// 2^-11 relative and the output's own is 2^-8.  For fp16 and fp32 they would show, so
-// K, V and P (and fp32 Q) are kept as fp16 hi + lo (NL = 2, 22 bits) and three products
-// are summed, hi hi + lo hi + hi lo, in the same fp32 accumulator.
+// The expanded values zero + scale c are rounded to fp16, bf16 and fp16 queries enter
+// exactly (scaled by a power of two per row), P is fp16.  For bf16 that is one product
+// each (NL = 1): those roundings are 2^-11 relative and the output's own is 2^-8.  For
+// fp16 and fp32 they would show, so K, V and P (and fp32 Q) are kept as fp16 hi + lo
+// (NL = 2, 22 bits) and three products are summed, hi hi + lo hi + hi lo, in the same
+// fp32 accumulator.
 //
 // Warp roles: warps 0-3 and 4-7 are two softmax streams, each with its own O
-// accumulator, so that neither waits for the other; a thread owns a row.  With
-// MT = 2 they are the two row tiles of the unit, and an expanded tile serves 256
-// rows; with MT = 1 (few rows, or fp32 at head_dim 128, whose query limbs leave no
-// shared memory) they take the even and the odd tiles and are merged at the unit's
-// end.  Warp 13 fills a ring of cache blocks (bulk copies), warps 8-11 expand them,
-// K and V of a tile in turn; warp 12 issues the mma (one thread): while one stream's
-// softmax works, the tensor core runs the other stream's products.  The mma of one
-// thread run in issue order, so a stream's next S cannot overwrite P before its O
-// has read it, and a completed S says that the stream's last O is done, which is
-// when it may be rescaled (the reference exponent moves only when it is exceeded by
-// 2^8).
+// accumulator and two score buffers; a thread owns a row.  With MT = 2 the streams
+// are the two row tiles of the unit, and an expanded tile serves 256 rows; with MT = 1
+// (few rows, or fp32 at head_dim 128, whose query limbs leave no shared memory) they
+// take the even and the odd tiles and are merged at the unit's end.  Warps 8-11
+// expand the blocks, K and V of a tile in turn, warp 13 fills their ring (bulk
+// copies), warp 12 issues the mma (one thread), the scores of the next tiles before
+// the values of this one, so that softmax and tensor core overlap.  The mma of one
+// thread run in issue order, so a score buffer is not overwritten before the product
+// with the weights in it has run.  The reference exponent moves only when it is
+// exceeded by 2^8; then O is rescaled, once the stream's last product is done.
 //
 // Work: the units' tiles (each unit only as far as its last row sees) laid end
 // to end, shared out evenly over one CTA per SM on the device, cut units merged
@@ -46,7 +44,7 @@
 namespace tqi {
 namespace {
 
-constexpr int kSoft = 256;                // softmax threads
+constexpr int kSoft = 256;                // softmax threads: two streams x 128 rows
 constexpr int kProd = 128;                // producer threads
 constexpr int kThreads = kSoft + kProd + 64;
 constexpr int kSlots = 6;                 // ring of raw cache blocks (64 tokens of K or of V)
@@ -55,16 +53,16 @@ constexpr float kRoom = 7.f, kLazy = 8.f; // P is kept below 2^15 (fp16 holds 65
 template <int D, int GRP, int NL, int QL, int MT>
 struct Ch {
     static constexpr int kNG = D / GRP;
-    static constexpr int TT = NL == 1 ? 128 : 64;             // tokens per tile
-    static constexpr int kBlks = TT / 64;                     // cache blocks per tile
+    static constexpr int TT = 64;                             // tokens per tile: one cache block
+    static constexpr int kBufs = NL == 1 ? 3 : 2;             // operand buffers
     static constexpr int kBlockB = 64 * (D / 2 + 4 * kNG);
     static constexpr int kTile = TT * D * 2;                  // one fp16 operand of a tile
     static constexpr int kQ = 128 * D * 2;                    // one limb of a row tile's queries
-    static constexpr int kBuf = 2 * NL * kTile;               // K limbs, V limbs; two buffers
-    static constexpr int kOffQ = 2 * kBuf;                    // [MT][QL]
+    static constexpr int kBuf = 2 * NL * kTile;               // K limbs, V limbs
+    static constexpr int kOffQ = kBufs * kBuf;                    // [MT][QL]
     static constexpr int kOffRing = kOffQ + MT * QL * kQ;
     static constexpr int kOffBar = kOffRing + kSlots * kBlockB;
-    static constexpr int kOffXch = kOffBar + 32 * 8;          // [2][2][128]: reference, sum
+    static constexpr int kOffXch = kOffBar + 38 * 8;          // [2][2][128]: reference, sum
     static constexpr int kOffBad = kOffXch + 4 * 128 * 4;     // [4 segments][4 groups]: first non-finite token
     static constexpr int kOffScan = kOffBad + 16 * 4;         // [kThreads / 32 + 3] int64
     static constexpr int kOffMisc = kOffScan + (kThreads / 32 + 3) * 8;
@@ -72,23 +70,26 @@ struct Ch {
     static_assert(kOffRing % 16 == 0 && kOffBar % 8 == 0 && kOffScan % 8 == 0, "alignment");
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
     // tensor memory columns
-    static constexpr int kX = 0;                              // S / P of stream x at TT x
-    static constexpr int kO = 2 * TT;                         // O of stream x at kO + D x
+    static constexpr int kX = 0;                              // S / P of stream x, buffer b at TT (2 x + b)
+    static constexpr int kO = 4 * TT;                         // O of stream x at kO + D x
     static_assert(kO + 2 * D <= 512, "tensor memory");
 };
 
+// mbarriers.  A barrier is never two phases ahead of a thread that waits on it: whatever a
+// stream's two score buffers allow to run ahead has a barrier per buffer.
 enum : int {
     kBarRing = 0,      // [6] a raw block in its slot (copy bytes)
     kBarSlot = 6,      // [6] a raw block read (kProd arrivals)
-    kBarKReady = 12,   // [2] K operand of a buffer built (kProd arrivals)
-    kBarVReady = 14,   // [2] V operand
-    kBarKFree = 16,    // [2] K operand read (commit)
-    kBarVFree = 18,    // [2] V operand read (commit)
-    kBarS = 20,        // [2] S of stream x computed (commit)
-    kBarP = 22,        // [2] P of stream x written (128 arrivals)
-    kBarSeg = 24,      // O of a segment complete (commit), and the mma thread's own arrival
-    kBarQ = 25,        // query operand written (256 arrivals)
-    kBarDrain = 26,    // every mma done (commit, at exit)
+    kBarKReady = 12,   // [3] K operand of a buffer built (kProd arrivals)
+    kBarVReady = 15,   // [3] V operand
+    kBarKFree = 18,    // [3] K operand read (commit)
+    kBarVFree = 21,    // [3] V operand read (commit)
+    kBarS = 24,        // [2][2] S of stream x, score buffer b computed (commit)
+    kBarP = 28,        // [2][2] P of stream x in score buffer b written (128 arrivals)
+    kBarO = 32,        // [2] O of stream x updated (commit)
+    kBarSeg = 34,      // O of a segment complete (commit), and the mma thread's own arrival
+    kBarQ = 35,        // query operand written (256 arrivals)
+    kBarDrain = 36,    // every mma done (commit, at exit)
 };
 
 // tokens that the last row of row tile rt sees, and the tiles they take (at least one)
@@ -128,6 +129,34 @@ struct Walk {
 
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
     return __all_sync(kFull, mbar_wait_bounded(bar, parity));
+}
+// mma and commit by the warp's elected lane, called by the whole warp: the operands are then
+// warp-uniform to the compiler and stay in uniform registers (one diverged thread issued an
+// mma every 80 to 100 clocks, more than it takes to run)
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\t"
+        "elect.sync r|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t.reg .b32 r;\n\t"
+        "elect.sync r|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t.reg .b32 r;\n\t"
+        "elect.sync r|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        : "memory");
 }
 // barrier over the softmax threads that ORs v
 __device__ __forceinline__ bool soft_or(bool v) {
@@ -279,13 +308,18 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             mbar_init(bar(kBarRing + i), 1);
             mbar_init(bar(kBarSlot + i), kProd);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < C::kBufs; ++i) {
             mbar_init(bar(kBarKReady + i), kProd);
             mbar_init(bar(kBarVReady + i), kProd);
             mbar_init(bar(kBarKFree + i), 1);
             mbar_init(bar(kBarVFree + i), 1);
-            mbar_init(bar(kBarS + i), 1);
-            mbar_init(bar(kBarP + i), 128);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(kBarO + i), 1);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(bar(kBarS + 2 * i + b), 1);
+                mbar_init(bar(kBarP + 2 * i + b), 128);
+            }
         }
         mbar_init(bar(kBarSeg), 2);
         mbar_init(bar(kBarQ), kSoft);
@@ -355,10 +389,13 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
 
     bool failed = false;
     if (warp < 8) {
-        // ======================================== softmax: stream x, thread = row r of its tile
+        // ======================================== softmax: stream x, thread = row r of its row tile
         const int x = warp >> 2, r = tid & 127;
         const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
         float* xch = reinterpret_cast<float*>(sm + C::kOffXch);
+        // values of a row that this thread loads and stores
+        constexpr int kCols = MT == 2 ? D : D / 2;
+        const int col0 = MT == 2 ? 0 : x * kCols;
         W w = w0;
         int seg = 0, nS = 0;                                  // segments, S of this stream so far
         for (int j = 0; j < J; ++seg) {
@@ -370,30 +407,28 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             const bool rvalid = grow < a.rows;
             const int64_t qi = rvalid ? grow / a.G : 0, qg = rvalid ? grow - qi * a.G : 0;
             const int64_t qrow = ((int64_t)w.b * a.Lq + qi) * a.Hq + (int64_t)w.kv * a.G + qg;
-            // (a row that is not there sees everything: no masking for it, and nothing of it is stored)
-            const int64_t lim = rvalid ? w.n - a.Lq + 1 + qi : INT64_MAX;
+            // tokens that the row sees, clamped to 32 bits (a row that is not there sees everything: no
+            // masking for it, and nothing of it is stored)
+            const int64_t lim64 = rvalid ? w.n - a.Lq + 1 + qi : INT_MAX;
+            const int lim = lim64 < 0 ? 0 : (int)lim64;
             // query operand: the row scaled by a power of two (largest element in [2^14, 2^15));
-            // with MT = 1 each stream does half of the values (position p of a word's eight
-            // holds value word_value(p), as the expanded operands do)
+            // position p of a word's eight holds value word_value(p), as in the expanded operands
             float fr;
             {
-                constexpr int NQ = MT == 2 ? D : D / 2;
-                const int q0 = MT == 2 ? 0 : x * (D / 2);
                 float mx = 0.f;
                 if (rvalid) {
 #pragma unroll
-                    for (int e0 = 0; e0 < NQ; e0 += 32) {
-                        float v[32];
-                        load_row<DT, 32>(a.q, qrow * D + q0 + e0, a.vec16, v);
+                    for (int e0 = 0; e0 < kCols; e0 += 16) {
+                        float v[16];
+                        load_row<DT, 16>(a.q, qrow * D + col0 + e0, a.vec16, v);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, fabsf(v[e]));
+                        for (int e = 0; e < 16; ++e) mx = fmaxf(mx, fabsf(v[e]));
                     }
                 }
                 if constexpr (MT == 1) {
                     xch[x * 128 + r] = mx;
                     soft_or(false);
                     mx = fmaxf(mx, xch[(x ^ 1) * 128 + r]);
-                    soft_or(false);
                 }
                 int ex = mx > 0.f ? ilogbf(mx) : 0;
                 ex = ex < -100 ? -100 : ex;
@@ -402,21 +437,21 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 fr = fmaxf(fabsf(a.scale_log2) / f, 1e-37f);  // (above zero: a masked -inf stays one)
                 uint8_t* sq = sm + C::kOffQ + (MT == 2 ? x * QL * C::kQ : 0);
 #pragma unroll 1
-                for (int c0 = 0; c0 < NQ; c0 += 32) {
-                    float v[32];
+                for (int c0 = 0; c0 < kCols; c0 += 16) {
+                    float v[16];
                     if (rvalid) {
-                        load_row<DT, 32>(a.q, qrow * D + q0 + c0, a.vec16, v);
+                        load_row<DT, 16>(a.q, qrow * D + col0 + c0, a.vec16, v);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                        for (int e = 0; e < 16; ++e) v[e] = 0.f;
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; i += 8) {          // eight positions, 16 bytes
+                    for (int i = 0; i < 16; i += 8) {          // eight positions, 16 bytes
                         uint32_t qh[4], qlo[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             split_hilo(v[i + word_value(2 * k)] * fs, v[i + word_value(2 * k + 1)] * fs, qh[k], qlo[k]);
-                        const uint32_t at = sw128_byte(r, 2 * (q0 + c0 + i), 128);
+                        const uint32_t at = sw128_byte(r, 2 * (col0 + c0 + i), 128);
                         *reinterpret_cast<uint4*>(sq + at) = make_uint4(qh[0], qh[1], qh[2], qh[3]);
                         if constexpr (QL == 2)
                             *reinterpret_cast<uint4*>(sq + C::kQ + at) = make_uint4(qlo[0], qlo[1], qlo[2], qlo[3]);
@@ -427,109 +462,97 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             }
             float mref = -INFINITY, lsum = 0.f;
             bool any = false;                                  // this stream has an O
-            const uint32_t tx = tl + C::kX + TT * x;
             const uint64_t fr2 = pack2(fr, fr);
             for (int jj = MT == 2 ? j : j + ((j & 1) ^ x); jj < j1 && !failed; jj += 3 - MT) {
-                const int64_t tok0 = (int64_t)(k0 + (jj - j)) * TT;
-                if (!warp_wait(bar(kBarS + x), (uint32_t)(nS & 1))) { failed = true; break; }
+                const int b = 2 * x + (nS & 1);                // score buffer
+                const uint32_t tx = tl + C::kX + TT * b;
+                const int64_t rest = (int64_t)lim - (int64_t)(k0 + (jj - j)) * TT;
+                const int vis = rest >= TT ? TT : (int)(rest > 0 ? rest : 0);
+                if (!warp_wait(bar(kBarS + b), (uint32_t)((nS >> 1) & 1))) { failed = true; break; }
                 ++nS;
                 tc_fence_after();
-                // 64 tokens at a time; P of tokens 2 i, 2 i + 1 goes to column i, over scores that
-                // have been read (NL = 2: low limbs to column 32 + i)
-#pragma unroll 1
-                for (int h = 0; h < TT / 64; ++h) {
-                    uint32_t sv[64];
-                    tc_ld64(tx + 64 * h, sv);
-                    const int64_t rest = lim - tok0 - 64 * h;
-                    const int vis = rest >= 64 ? 64 : (int)(rest > 0 ? rest : 0);
-                    if (vis < 64) {
+                uint32_t sv[TT];
+                tc_ld64(tx, sv);
+                if (vis < TT) {
 #pragma unroll
-                        for (int t = 0; t < 64; ++t)
-                            if (t >= vis) sv[t] = 0xff800000u;
+                    for (int t = 0; t < TT; ++t)
+                        if (t >= vis) sv[t] = 0xff800000u;
+                }
+                // P = 2^(S fr - mref) over S (tokens 2 i, 2 i + 1 in column i; NL = 2: low limbs in
+                // column 32 + i), and its sum; 16 tokens at a time (fewer registers)
+                float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                auto weights = [&](float m) -> float {
+                    const uint64_t m2 = pack2(-m, -m);
+                    uint64_t sum2[2] = {0ull, 0ull};
+#pragma unroll
+                    for (int qt = 0; qt < 4; ++qt) {
+                        uint32_t ph[8], pl[8];
+#pragma unroll
+                        for (int t = 0; t < 16; t += 2) {
+                            const float a0 = __uint_as_float(sv[16 * qt + t]), a1 = __uint_as_float(sv[16 * qt + t + 1]);
+                            mx4[(t >> 1) & 3] = fmaxf(mx4[(t >> 1) & 3], fmaxf(a0, a1));
+                            float e0, e1;
+                            unpack2(fma2(pack2(a0, a1), fr2, m2), e0, e1);
+                            e0 = fast_exp2(e0);
+                            e1 = fast_exp2(e1);
+                            sum2[(t >> 1) & 1] = add2(sum2[(t >> 1) & 1], pack2(e0, e1));
+                            if constexpr (NL == 2) split_hilo(e0, e1, ph[t >> 1], pl[t >> 1]);
+                            else ph[t >> 1] = h2_bits(__floats2half2_rn(e0, e1));
+                        }
+                        tc_st8(tx + 8 * qt, ph);
+                        if constexpr (NL == 2) tc_st8(tx + 32 + 8 * qt, pl);
                     }
-                    // P = 2^(S fr - mref) and its sum; 16 tokens at a time (fewer registers)
-                    float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    auto weights = [&](float m) -> float {
-                        const uint64_t m2 = pack2(-m, -m);
-                        uint64_t sum2[2] = {0ull, 0ull};
-#pragma unroll
-                        for (int qt = 0; qt < 4; ++qt) {
-                            uint32_t ph[8], pl[8];
-#pragma unroll
-                            for (int t = 0; t < 16; t += 2) {
-                                const float a0 = __uint_as_float(sv[16 * qt + t]), a1 = __uint_as_float(sv[16 * qt + t + 1]);
-                                mx4[(t >> 1) & 3] = fmaxf(mx4[(t >> 1) & 3], fmaxf(a0, a1));
-                                float e0, e1;
-                                unpack2(fma2(pack2(a0, a1), fr2, m2), e0, e1);
-                                e0 = fast_exp2(e0);
-                                e1 = fast_exp2(e1);
-                                sum2[(t >> 1) & 1] = add2(sum2[(t >> 1) & 1], pack2(e0, e1));
-                                if constexpr (NL == 2) split_hilo(e0, e1, ph[t >> 1], pl[t >> 1]);
-                                else ph[t >> 1] = h2_bits(__floats2half2_rn(e0, e1));
-                            }
-                            tc_st8(tx + 32 * h + 8 * qt, ph);
-                            if constexpr (NL == 2) tc_st8(tx + 32 + 8 * qt, pl);
-                        }
-                        float s0, s1;
-                        unpack2(add2(sum2[0], sum2[1]), s0, s1);
-                        return s0 + s1;
-                    };
-                    // The weights are taken with the reference as it is, the maximum beside them (off the
-                    // critical path); where the reference turns out exceeded by 2^kLazy (always in a unit's
-                    // first tile) it moves, O and the tile's earlier weights are rescaled by whole warps, and
-                    // the weights are taken again.
-                    float sum = weights(mref == -INFINITY ? 0.f : mref);
-                    const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fr;
-                    const bool move = mx - kRoom - kLazy > mref;
-                    if (__any_sync(kFull, move)) {
-                        float f = 1.f;
-                        if (move) {
-                            f = mref == -INFINITY ? 0.f : fast_exp2(mref - (mx - kRoom));
-                            mref = mx - kRoom;
-                            lsum *= f;
-                        }
-                        if (any) {
-#pragma unroll 1
-                            for (int c0 = 0; c0 < D; c0 += 16) {
-                                uint32_t ov[16];
-                                tc_ld16(tl + C::kO + D * x + c0, ov);
-#pragma unroll
-                                for (int cc = 0; cc < 16; ++cc) ov[cc] = __float_as_uint(__uint_as_float(ov[cc]) * f);
-                                tc_st16(tl + C::kO + D * x + c0, ov);
-                            }
-                        }
-                        if (h > 0) {
-                            tc_wait_st();
-                            const __half2 f2 = __float2half2_rn(f);
-#pragma unroll 1
-                            for (int c0 = 0; c0 < 32 * h; c0 += 16) {
-                                uint32_t pv[16];
-                                tc_ld16(tx + c0, pv);
-#pragma unroll
-                                for (int cc = 0; cc < 16; ++cc) pv[cc] = f == 0.f ? 0u : h2_bits(__hmul2(as_h2(pv[cc]), f2));
-                                tc_st16(tx + c0, pv);
-                            }
-                        }
-                        sum = weights(mref == -INFINITY ? 0.f : mref);
+                    float s0, s1;
+                    unpack2(add2(sum2[0], sum2[1]), s0, s1);
+                    return s0 + s1;
+                };
+                // The weights are taken with the reference as it is, the maximum beside them (off the
+                // critical path); where the reference turns out exceeded by 2^kLazy (always in a unit's
+                // first tile) it moves, O is rescaled by whole warps and the weights are taken again.
+                float sum = weights(mref == -INFINITY ? 0.f : mref);
+                const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * fr;
+                const bool move = mx - kRoom - kLazy > mref;
+                if (__any_sync(kFull, move)) {
+                    float f = 1.f;
+                    if (move) {
+                        f = mref == -INFINITY ? 0.f : fast_exp2(mref - (mx - kRoom));
+                        mref = mx - kRoom;
+                        lsum *= f;
                     }
-                    lsum += sum;
+                    if (any) {
+                        // the product with the stream's tile before (its product nS - 2) is done
+                        if (!warp_wait(bar(kBarO + x), (uint32_t)(nS & 1))) { failed = true; break; }
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c0 = 0; c0 < D; c0 += 16) {
+                            uint32_t ov[16];
+                            tc_ld16(tl + C::kO + D * x + c0, ov);
+#pragma unroll
+                            for (int cc = 0; cc < 16; ++cc) ov[cc] = __float_as_uint(__uint_as_float(ov[cc]) * f);
+                            tc_st16(tl + C::kO + D * x + c0, ov);
+                        }
+                    }
+                    sum = weights(mref == -INFINITY ? 0.f : mref);
                 }
                 any = true;
+                lsum += sum;
                 tc_wait_st();
                 tc_fence_before();
-                mbar_arrive(bar(kBarP + x));
+                mbar_arrive(bar(kBarP + b));
             }
             // ---- the segment's end
             if (!failed && !warp_wait(bar(kBarSeg), (uint32_t)(seg & 1))) failed = true;
             tc_fence_after();
             if (!any) mref = -INFINITY;
-            if (lsum != lsum && mref == -INFINITY) mref = 0.f;   // nothing but NaN scores
             // groups with a non-finite pair on a token that this row sees
             uint32_t bad = 0;
 #pragma unroll
-            for (int g = 0; g < NG; ++g) bad |= (uint32_t)((int64_t)sBad[4 * (seg & 3) + g] < lim) << g;
-            xch[x * 128 + r] = mref;
-            xch[(2 + x) * 128 + r] = lsum;
+            for (int g = 0; g < NG; ++g) bad |= (uint32_t)(sBad[4 * (seg & 3) + g] < lim) << g;
+            if (lsum != lsum && mref == -INFINITY) mref = 0.f;   // nothing but NaN scores
+            if constexpr (MT == 1) {
+                xch[x * 128 + r] = mref;
+                xch[(2 + x) * 128 + r] = lsum;
+            }
             if (soft_or(failed)) failed = true;
             const bool begins = k0 == 0, ends = j1 - j == left, whole = begins && ends;
             const int64_t slot = (2 * c + (begins ? 1 : 0)) * ROWS + ur;
@@ -545,18 +568,17 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             const float f0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - mm), f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - mm);
             const float L = mm == -INFINITY ? 0.f : (f0 == 0.f ? 0.f : f0 * l0) + (f1 == 0.f ? 0.f : f1 * l1);
             const float inv = whole && mm != -INFINITY ? 1.f / L : 1.f;
-            constexpr int kCols = MT == 2 ? D : D / 2;
 #pragma unroll 1
-            for (int c0 = 0; c0 < kCols; c0 += 32) {
-                const int col = MT == 2 ? c0 : x * (D / 2) + c0;
-                uint32_t o0[32], o1[32];
-                tc_ld32(tl + C::kO + (MT == 2 ? D * x : 0) + col, o0);
-                if constexpr (MT == 1) tc_ld32(tl + C::kO + D + col, o1);
-                const bool poison = (bad >> (col / GRP)) & 1u; // (a run of 32 lies in one group)
+            for (int c0 = 0; c0 < kCols; c0 += 16) {
+                const int col = col0 + c0;
+                uint32_t o0[16], o1[16];
+                tc_ld16(tl + C::kO + (MT == 2 ? D * x : 0) + col, o0);
+                if constexpr (MT == 1) tc_ld16(tl + C::kO + D + col, o1);
+                const bool poison = (bad >> (col / GRP)) & 1u; // (a run of 16 lies in one group)
                 if (!rvalid) continue;
-                float v[32];
+                float v[16];
 #pragma unroll
-                for (int cc = 0; cc < 32; ++cc) {
+                for (int cc = 0; cc < 16; ++cc) {
                     float y = 0.f;
                     if (mm != -INFINITY) {
                         if (f0 != 0.f) y = __uint_as_float(o0[cc]) * f0;
@@ -567,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                     v[(cc & ~7) + word_value(cc & 7)] = y * inv;
                 }
 #pragma unroll
-                for (int i = 0; i < 32; i += 8) {
+                for (int i = 0; i < 16; i += 8) {
                     const float u[8] = {v[i], v[i + 1], v[i + 2], v[i + 3], v[i + 4], v[i + 5], v[i + 6], v[i + 7]};
                     if (whole) store8<DT>(a.out, qrow * D + col + i, a.vec16, u);
                     else store8<TQ_F32>(a.part_acc, slot * D + col + i, true, u);
@@ -583,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 a.split[c] = make_int4(w.b, w.rt * (int)a.Hkv + w.kv, (int)((end * nC - 1) / N), 1);
             }
             // the next segment's queries and exchange overwrite what was read here (the marks of
-            // this segment's slot are next used four segments on; producers are at most two ahead)
+            // this segment's slot are next used four segments on; producers are at most three ahead)
             if (tid < 4) sBad[4 * (seg & 3) + tid] = INT_MAX;
             tc_fence_before();
             soft_or(false);
@@ -594,8 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
         }
         if (failed) atomicExch(a.err, 1);
     } else if (warp < 12) {
-        // ======================================== producers: thread = token `tau0` (D = 128: and
-        // tau0 + 32) of piece cp (32 values) of a block
+        // ======================================== producers: K, then V block of a tile; thread =
+        // token `tau0` (D = 128: and tau0 + 32) of piece cp (32 values)
         const int pw = warp - 8;
         W w = w0;
         constexpr int kPieces = D / 32, kItems = 64 * kPieces / kProd;   // items per block and thread
@@ -607,92 +629,83 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < 4; ++i) at[i] = sw128_byte(tau0, 2 * (32 * cp + 8 * i), TT);
         int slot = 0, sp = 0, bf = 0, bfp = 0, seg = 0;        // ring slot and buffer, with their phases
-        for (int j = 0; j < J && !failed; ++j) {
-#pragma unroll 1
-            for (int side = 0; side < 2 && !failed; ++side) {  // K, then V
-                if (j >= 2 && !warp_wait(bar((side ? kBarVFree : kBarKFree) + bf), (uint32_t)(bfp ^ 1))) { failed = true; break; }
-#pragma unroll 1
-                for (int blk = 0; blk < C::kBlks; ++blk) {
-                    if (!warp_wait(bar(kBarRing + slot), (uint32_t)sp)) { failed = true; break; }
-                    const uint8_t* raw_blk = sm + C::kOffRing + slot * C::kBlockB;
-                    const int64_t tok0 = (int64_t)w.k * TT + 64 * blk, inside = w.n - tok0;
-                    const int valid = inside < 64 ? (int)(inside > 0 ? inside : 0) : 64;   // tokens inside the sequence
-                    uint4 v[kItems];
-                    uint32_t bits[kItems];
-                    bool rare = false;
+        for (int i = 0; i < 2 * J; ++i) {
+            const int side = i & 1;                            // 0: K, 1: V
+            if (!warp_wait(bar(kBarRing + slot), (uint32_t)sp)) { failed = true; break; }
+            const uint8_t* raw_blk = sm + C::kOffRing + slot * C::kBlockB;
+            const int64_t tok0 = (int64_t)w.k * TT, inside = w.n - tok0;
+            const int valid = inside < TT ? (int)(inside > 0 ? inside : 0) : TT;           // tokens inside the sequence
+            uint4 v[kItems];
+            uint32_t bits[kItems];
+            bool rare = false;
 #pragma unroll
-                    for (int it = 0; it < kItems; ++it) {
-                        v[it] = *reinterpret_cast<const uint4*>(raw_blk + src + 32 * it * (D / 2));
-                        bits[it] = *reinterpret_cast<const uint32_t*>(raw_blk + prs + 32 * it * NG * 4);
-                        // behind the sequence anything may stand
-                        if (tau0 + 32 * it >= valid) bits[it] = 0u;
-                        // a scale of 2^11 or more, a zero of 2^15 or more, infinity or NaN
-                        rare |= (bits[it] & 0x7fffu) >= 0x6800u || (bits[it] & 0x7fff0000u) >= 0x78000000u;
-                    }
-                    if (rare) {
-#pragma unroll
-                        for (int it = 0; it < kItems; ++it) {
-                            if (side && ((bits[it] & 0x7c00u) == 0x7c00u || (bits[it] & 0x7c000000u) == 0x7c000000u)) {
-                                bits[it] = 0u;
-                                atomicMin(&sBad[4 * (seg & 3) + gam], (int)tok0 + tau0 + 32 * it);
-                            }
-                            // the largest value stays finite in fp16
-                            if (fmaf(15.f, __low2float(as_h2(bits[it])), __high2float(as_h2(bits[it]))) > 65504.f) bits[it] -= 1u;
-                        }
-                    }
-                    uint8_t* buf = sm + bf * C::kBuf + side * NL * C::kTile + blk * 64 * 128;
-#pragma unroll
-                    for (int it = 0; it < kItems; ++it) {
-                        const __half2 s2 = __low2half2(as_h2(bits[it])), z2 = __high2half2(as_h2(bits[it]));
-                        const uint32_t wd[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
-                        uint8_t* op = buf + 32 * it * 128;     // (32 rows further: 4 atoms of 1024 bytes)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t h[4], l[4];
-                            expand_word<NL>(wd[i], s2, z2, h, l);
-                            *reinterpret_cast<uint4*>(op + at[i]) = make_uint4(h[0], h[1], h[2], h[3]);
-                            if constexpr (NL == 2)
-                                *reinterpret_cast<uint4*>(op + C::kTile + at[i]) = make_uint4(l[0], l[1], l[2], l[3]);
-                        }
-                    }
-                    fence_proxy_async();   // operands for the tensor core; the slot's reads before its next copy
-                    mbar_arrive(bar(kBarSlot + slot));
-                    if (++slot == kSlots) { slot = 0; sp ^= 1; }
-                }
-                if (!failed) mbar_arrive(bar((side ? kBarVReady : kBarKReady) + bf));
+            for (int it = 0; it < kItems; ++it) {
+                v[it] = *reinterpret_cast<const uint4*>(raw_blk + src + 32 * it * (D / 2));
+                bits[it] = *reinterpret_cast<const uint32_t*>(raw_blk + prs + 32 * it * NG * 4);
+                if (tau0 + 32 * it >= valid) bits[it] = 0u;    // behind the sequence anything may stand
+                // a scale of 2^11 or more, a zero of 2^15 or more, infinity or NaN
+                rare |= (bits[it] & 0x7fffu) >= 0x6800u || (bits[it] & 0x7fff0000u) >= 0x78000000u;
             }
-            if ((bf ^= 1) == 0) bfp ^= 1;
+            if (i >= 2 * C::kBufs && !warp_wait(bar((side ? kBarVFree : kBarKFree) + bf), (uint32_t)(bfp ^ 1))) {
+                failed = true;
+                break;
+            }
+            if (rare) {                                        // (after the wait: it bounds how far ahead marks are made)
+#pragma unroll
+                for (int it = 0; it < kItems; ++it) {
+                    if (side && ((bits[it] & 0x7c00u) == 0x7c00u || (bits[it] & 0x7c000000u) == 0x7c000000u)) {
+                        bits[it] = 0u;
+                        atomicMin(&sBad[4 * (seg & 3) + gam], (int)tok0 + tau0 + 32 * it);
+                    }
+                    // the largest value stays finite in fp16
+                    if (fmaf(15.f, __low2float(as_h2(bits[it])), __high2float(as_h2(bits[it]))) > 65504.f) bits[it] -= 1u;
+                }
+            }
+            uint8_t* buf = sm + bf * C::kBuf + side * NL * C::kTile;
+#pragma unroll
+            for (int it = 0; it < kItems; ++it) {
+                const __half2 s2 = __low2half2(as_h2(bits[it])), z2 = __high2half2(as_h2(bits[it]));
+                const uint32_t wd[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
+                uint8_t* op = buf + 32 * it * 128;             // (32 rows further: 4 atoms of 1024 bytes)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t h[4], l[4];
+                    expand_word<NL>(wd[i], s2, z2, h, l);
+                    *reinterpret_cast<uint4*>(op + at[i]) = make_uint4(h[0], h[1], h[2], h[3]);
+                    if constexpr (NL == 2) *reinterpret_cast<uint4*>(op + C::kTile + at[i]) = make_uint4(l[0], l[1], l[2], l[3]);
+                }
+            }
+            fence_proxy_async();           // operands for the tensor core; the slot's reads before its next copy
+            mbar_arrive(bar(kBarSlot + slot));
+            mbar_arrive(bar((side ? kBarVReady : kBarKReady) + bf));
+            if (++slot == kSlots) { slot = 0; sp ^= 1; }
+            if (!side) continue;
+            if (++bf == C::kBufs) { bf = 0; bfp ^= 1; }
             if (w.k == w.nt - 1) ++seg;
             w.next(a);
         }
         if (failed && lane == 0) atomicExch(a.err, 1);
     } else if (warp == 13) {
-        // ======================================== loader: one thread fills the ring, per tile the K
-        // blocks and then the V blocks
+        // ======================================== loader: one thread fills the ring, K and V block
+        // of each tile
         if (lane == 0) {
             W w = w0;
             int i = 0, slot = 0, sp = 0;                       // blocks loaded
             asm volatile("fence.proxy.async;" ::: "memory");
             for (int j = 0; j < J && !failed; ++j) {
                 const int64_t bh = (int64_t)w.b * a.Hkv + w.kv;
-                int64_t blk[2 * C::kBlks];
-#pragma unroll
-                for (int k = 0; k < 2 * C::kBlks; ++k) {
-                    // (a tile may reach behind the last block: that one again, its tokens count as absent)
-                    const int64_t last = w.n > 0 ? (w.n - 1) >> 6 : 0, lb = (int64_t)w.k * C::kBlks + k % C::kBlks;
-                    const bool v = k >= C::kBlks;
-                    const int64_t p = w.n > 0 ? cache_block(v ? a.vtable : a.ktable, v ? a.vpool : a.kpool, a.NB, bh,
-                                                            lb < last ? lb : last, a.err)
-                                              : 0;
-                    blk[k] = p >= 0 ? p : 0;                   // a bad table entry reads block 0
+                int64_t blk[2] = {0, 0};                       // (an empty sequence reads block 0, all masked)
+                if (w.n > 0) {
+                    blk[0] = cache_block(a.ktable, a.kpool, a.NB, bh, w.k, a.err);
+                    blk[1] = cache_block(a.vtable, a.vpool, a.NB, bh, w.k, a.err);
                 }
 #pragma unroll
-                for (int k = 0; k < 2 * C::kBlks; ++k) {
+                for (int k = 0; k < 2; ++k) {
                     if (i >= kSlots && !mbar_wait_bounded(bar(kBarSlot + slot), (uint32_t)(sp ^ 1))) { failed = true; break; }
                     const uint32_t br = bar(kBarRing + slot);
                     mbar_expect_tx(br, (uint32_t)C::kBlockB);
-                    bulk_g2s(smem_u32(sm + C::kOffRing + slot * C::kBlockB),
-                             (k >= C::kBlks ? a.vc : a.kc) + blk[k] * C::kBlockB, C::kBlockB, br);
+                    bulk_g2s(smem_u32(sm + C::kOffRing + slot * C::kBlockB),               // a bad table entry reads block 0
+                             (k ? a.vc : a.kc) + (blk[k] >= 0 ? blk[k] : 0) * C::kBlockB, C::kBlockB, br);
                     ++i;
                     if (++slot == kSlots) { slot = 0; sp ^= 1; }
                 }
@@ -703,8 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 mbar_wait_bounded(bar(kBarRing + k % kSlots), (uint32_t)((k / kSlots) & 1));
             if (failed) atomicExch(a.err, 1);
         }
-    } else if (lane == 0) {
-        // ======================================== the mma thread
+    } else {
+        // ======================================== the mma warp (uniform; its elected lane issues)
         constexpr uint32_t kIdS = idesc_f16(128, TT), kIdO = idesc_f16_bmn(128, D);
         W w = w0;
         bool ok = true;
@@ -712,12 +725,13 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
         // shared-memory addresses are below 2^18, so it does not carry)
         const uint64_t qdesc = sw128_desc(sbase + C::kOffQ), kdesc = sw128_desc(sbase);
         const uint64_t vdesc = sw128_desc_mn(sbase + NL * C::kTile, (uint32_t)(TT * 128), 1024u);
-        int nP[2] = {0, 0};                // P of each stream waited for so far
+        int nS[2] = {0, 0}, nP[2] = {0, 0};    // S issued and P taken of each stream so far
         // S of stream x from buffer bf
         auto mma_s = [&](int x, int bf, bool last) {
             const uint64_t kd = kdesc + (uint64_t)(bf * (C::kBuf >> 4));
             const uint64_t qd = qdesc + (uint64_t)(MT == 2 ? x * ((QL * C::kQ) >> 4) : 0);
-            const uint32_t xd = tmem + C::kX + TT * x;
+            const int b = 2 * x + (nS[x]++ & 1);                // score buffer
+            const uint32_t xd = tmem + C::kX + TT * b;
             uint32_t acc = 0u;
 #pragma unroll
             for (int pr = 0; pr < 3; ++pr) {                   // hi hi, lo hi, hi lo
@@ -725,21 +739,21 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 const uint32_t ql = pr == 1 ? (uint32_t)C::kQ : 0u, kl = pr == 2 ? (uint32_t)C::kTile : 0u;
 #pragma unroll
                 for (int s = 0; s < D / 16; ++s) {
-                    tc_mma_f16_ss(xd, qd + ((ql + (uint32_t)((s >> 2) * (128 * 128) + (s & 3) * 32)) >> 4),
+                    mma_ss(xd, qd + ((ql + (uint32_t)((s >> 2) * (128 * 128) + (s & 3) * 32)) >> 4),
                                   kd + ((kl + (uint32_t)((s >> 2) * (TT * 128) + (s & 3) * 32)) >> 4), kIdS, acc);
                     acc = 1u;
                 }
             }
-            tc_commit(bar(kBarS + x));
-            if (last) tc_commit(bar(kBarKFree + bf));          // the tile's last use of K
+            commit(bar(kBarS + b));
+            if (last) commit(bar(kBarKFree + bf));          // the tile's last use of K
         };
-        // O of stream x (+)= P V from buffer bf, once P (and V) are there
-        auto mma_o = [&](int x, int bf, uint32_t vphase, bool first, bool last) -> bool {
-            if (!mbar_wait_bounded(bar(kBarVReady + bf), vphase)) return false;
-            if (!mbar_wait_bounded(bar(kBarP + x), (uint32_t)(nP[x] & 1))) return false;
+        // O of stream x (+)= P V from buffer bf, once P is there
+        auto mma_o = [&](int x, int bf, bool first, bool last) -> bool {
+            const int b = 2 * x + (nP[x] & 1);                  // score buffer
+            if (!warp_wait(bar(kBarP + b), (uint32_t)((nP[x] >> 1) & 1))) return false;
             ++nP[x];
+            const uint32_t od = tmem + C::kO + D * x, pa = tmem + C::kX + TT * b;
             tc_fence_after();
-            const uint32_t od = tmem + C::kO + D * x, pa = tmem + C::kX + TT * x;
             const uint64_t vd = vdesc + (uint64_t)(bf * (C::kBuf >> 4));
             uint32_t acc = first ? 0u : 1u;
 #pragma unroll
@@ -747,59 +761,57 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 const uint32_t pl = pr == 1 ? 32u : 0u, vl = pr == 2 ? (uint32_t)C::kTile : 0u;
 #pragma unroll
                 for (int s = 0; s < TT / 16; ++s) {
-                    tc_mma_f16_ts(od, pa + pl + 8 * s, vd + ((vl + 2048 * s) >> 4), kIdO, acc);
+                    mma_ts(od, pa + pl + 8 * s, vd + ((vl + 2048 * s) >> 4), kIdO, acc);
                     acc = 1u;
                 }
             }
-            if (last) tc_commit(bar(kBarVFree + bf));          // the tile's last use of V
+            commit(bar(kBarO + x));
+            if (last) commit(bar(kBarVFree + bf));          // the tile's last use of V
             return true;
         };
-        int seg = 0, jseg = 0;             // segments begun, first tile of this one
-        int pend = -1, pend_buf = 0;       // tile whose O (MT = 2: of stream 1) is still to be issued
-        uint32_t pend_phase = 0;
-        bool pend_first = false;
-        auto flush = [&]() -> bool {
-            if (pend < 0) return true;
-            const bool r = mma_o(MT == 2 ? 1 : pend & 1, pend_buf, pend_phase, pend_first, true);
-            pend = -1;
-            return r;
-        };
-        auto segment_done = [&]() {
-            tc_commit(bar(kBarSeg));
-            mbar_arrive(bar(kBarSeg));     // (orders what the producers noted, seen through their arrivals)
-        };
-        int bf = 0, bfp = 0;
-        for (int j = 0; j < J; ++j) {
-            if (j == 0 || w.k == 0) {      // a new unit: its queries replace the last one's
-                if (!(ok = flush())) break;
-                if (j > 0) segment_done();
-                if (!(ok = mbar_wait_bounded(bar(kBarQ), (uint32_t)(seg & 1)))) break;
-                ++seg;
-                jseg = j;
-            }
-            if (!(ok = mbar_wait_bounded(bar(kBarKReady + bf), (uint32_t)bfp))) break;
+        // S of tile j (both row tiles, or the tile's stream), once K is there
+        constexpr int kAhead = MT == 2 ? 1 : 2;                // tiles whose scores go out before this one's values
+        int sb = 0, sbp = 0;               // next K buffer and its phase
+        auto scores = [&](int j) -> bool {
+            if (!warp_wait(bar(kBarKReady + sb), (uint32_t)sbp)) return false;
             tc_fence_after();
-            mma_s(MT == 2 ? 0 : j & 1, bf, MT == 1);
-            if (!(ok = flush())) break;    // the other stream's last O
             if constexpr (MT == 2) {
-                mma_s(1, bf, true);
-                if (!(ok = mma_o(0, bf, (uint32_t)bfp, j == jseg, false))) break;
-                pend_first = j == jseg;
+                mma_s(0, sb, false);
+                mma_s(1, sb, true);
             } else {
-                pend_first = j - jseg < 2;
+                mma_s(j & 1, sb, true);
             }
-            pend = j;
-            pend_buf = bf;
-            pend_phase = (uint32_t)bfp;
+            if (++sb == C::kBufs) { sb = 0; sbp ^= 1; }
+            return true;
+        };
+        int vb = 0, vbp = 0;               // next V buffer and its phase
+        for (int j = 0, seg = 0; j < J && ok; ++seg) {
+            const int left = w.nt - w.k, j1 = j + left < J ? j + left : J;     // the segment's tiles
+            if (!(ok = warp_wait(bar(kBarQ), (uint32_t)(seg & 1)))) break;
+            for (int i = 0; i < kAhead && j + i < j1 && ok; ++i) ok = scores(j + i);
+            for (int i = j; i < j1 && ok; ++i) {
+                if (i + kAhead < j1 && !(ok = scores(i + kAhead))) break;
+                if (!(ok = warp_wait(bar(kBarVReady + vb), (uint32_t)vbp))) break;
+                if constexpr (MT == 2) {
+                    if (!(ok = mma_o(0, vb, i == j, false))) break;
+                    if (!(ok = mma_o(1, vb, i == j, true))) break;
+                } else {
+                    if (!(ok = mma_o(i & 1, vb, i - j < 2, true))) break;
+                }
+                if (++vb == C::kBufs) { vb = 0; vbp ^= 1; }
+            }
+            if (ok) {
+                commit(bar(kBarSeg));
+                if (lane == 0) mbar_arrive(bar(kBarSeg));      // (orders what the producers noted, seen through their arrivals)
+            }
+            w.k = w.nt - 1;
             w.next(a);
-            if ((bf ^= 1) == 0) bfp ^= 1;
+            j = j1;
         }
-        if (ok) ok = flush();
-        if (ok) segment_done();
         // every mma is done before tensor memory is released
-        tc_commit(bar(kBarDrain));
-        mbar_wait_bounded(bar(kBarDrain), 0u);
-        if (!ok) atomicExch(a.err, 1);
+        commit(bar(kBarDrain));
+        warp_wait(bar(kBarDrain), 0u);
+        if (!ok && lane == 0) atomicExch(a.err, 1);
     }
     pdl_trigger();
     tc_fence_before();
