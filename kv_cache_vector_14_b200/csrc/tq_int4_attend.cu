@@ -63,8 +63,8 @@ struct Shape {
     static constexpr int kOffQs = kOffFrag + (D == 256 ? NT * (D / 16) * 32 * 8 : 0);   // [kRows][kNG]
     static constexpr int kOffF = kOffQs + kRows * kNG * 4;                // [kRows]
     static constexpr int kOffMl = kOffF + kRows * 4;                      // [NW][kRows][2]
-    static constexpr int kOffDesc = (kOffMl + kNW * kRows * 8 + 15) / 16 * 16;   // [NW][kRing] int4
-    static constexpr int kOffBar = kOffDesc + kNW * kRing * 16;
+    static constexpr int kOffDesc = kOffMl + kNW * kRows * 8;             // [NW][kRing] int
+    static constexpr int kOffBar = (kOffDesc + kNW * kRing * 4 + 7) / 8 * 8;
     static constexpr int kOffScan = kOffBar + kNW * kRing * 8;            // [NW + 3] int64
     static constexpr int kSmem = kOffScan + (kNW + 3) * 8;
     static_assert(kOffKp % 16 == 0 && kOffVc % 16 == 0 && kOffVp % 16 == 0 && kStageB % 16 == 0, "bulk copies");
@@ -125,9 +125,11 @@ __device__ __forceinline__ void cursor_to(const Int4AttendArgs& a, int64_t units
 template <int D, int GRP>
 struct Words {
     static constexpr int kK = GRP / 32;                       // words per token and group, K side
-    // K: words j of group gam of token tok for lane quarter t
-    static __device__ __forceinline__ void key(const uint8_t* codes, int tok, int gam, int t, uint32_t (&w)[kK]) {
-        const uint8_t* p = codes + tok * (D / 2) + ((gam * (GRP / 2) + t * (GRP / 8)) ^ int4_swizzle(D, tok));
+    // K: words of group gam of token tok for lane quarter t, from byte key_at of the token codes
+    static __device__ __forceinline__ int key_at(int tok, int gam, int t) {
+        return tok * (D / 2) + ((gam * (GRP / 2) + t * (GRP / 8)) ^ int4_swizzle(D, tok));
+    }
+    static __device__ __forceinline__ void key(const uint8_t* p, uint32_t (&w)[kK]) {
         if constexpr (kK == 1) w[0] = *reinterpret_cast<const uint32_t*>(p);
         else if constexpr (kK == 2) {
             const uint2 v = *reinterpret_cast<const uint2*>(p);
@@ -139,8 +141,10 @@ struct Words {
     }
     // V: the GRP / 8 values of group gam that lane row g holds of token tok: 1 or 2 words, or a halfword
     static constexpr int kV = GRP == 128 ? 2 : 1;
-    static __device__ __forceinline__ void value(const uint8_t* codes, int tok, int gam, int g, uint32_t (&w)[kV]) {
-        const uint8_t* p = codes + tok * (D / 2) + ((gam * (GRP / 2) + g * (GRP / 16)) ^ int4_swizzle(D, tok));
+    static __device__ __forceinline__ int value_at(int tok, int gam, int g) {
+        return tok * (D / 2) + ((gam * (GRP / 2) + g * (GRP / 16)) ^ int4_swizzle(D, tok));
+    }
+    static __device__ __forceinline__ void value(const uint8_t* p, uint32_t (&w)[kV]) {
         if constexpr (GRP == 32) w[0] = *reinterpret_cast<const uint16_t*>(p);
         else if constexpr (GRP == 64) w[0] = *reinterpret_cast<const uint32_t*>(p);
         else {
@@ -153,9 +157,15 @@ struct Words {
 __device__ __forceinline__ uint32_t pick(uint32_t w, uint32_t w8, int r) {
     return (r < 2 ? w : w8) & ((r & 1) ? 0x00f000f0u : 0x000f000fu);
 }
-// the same with 15 - c in the high half (an odd token's value; see the kernel's value step)
-__device__ __forceinline__ uint32_t pick_odd(uint32_t w, uint32_t w8, int r) {
-    return pick(w, w8, r) ^ ((r & 1) ? 0x00f00000u : 0x000f0000u);
+// pool block of a block-table entry (contiguous cache: the row itself); bad: -1 and the check word
+__device__ __forceinline__ int64_t table_entry(const int32_t* table, int64_t pool, int64_t row, int* err) {
+    if (!table) return row;
+    const int32_t p = __ldg(table + row);
+    if (p < 0 || (int64_t)p >= pool) {
+        atomicExch(err, 1);
+        return -1;
+    }
+    return p;
 }
 
 template <int D, int GRP, int NT, int DT>
@@ -175,13 +185,13 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
     float* sQs = reinterpret_cast<float*>(smem + S::kOffQs);
     float* sF = reinterpret_cast<float*>(smem + S::kOffF);
     float* sMl = reinterpret_cast<float*>(smem + S::kOffMl);
-    int4* sDesc = reinterpret_cast<int4*>(smem + S::kOffDesc);
+    int* sDesc = reinterpret_cast<int*>(smem + S::kOffDesc);
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::kOffBar);
     int64_t* sScan = reinterpret_cast<int64_t*>(smem + S::kOffScan);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int gr = lane >> 2, tq4 = lane & 3;
     uint8_t* ring = smem + (size_t)warp * RING * S::kStageB;
-    int4* desc = sDesc + warp * RING;
+    int* desc = sDesc + warp * RING;                          // first token of each stage's chunk
     uint64_t* bar = bars + warp * RING;
 
     if (lane == 0)
@@ -253,24 +263,44 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
 
     // ---------------- the ring: this warp's chunks are lo + warp, lo + warp + NW, ...
     const int nmine = hi - lo > warp ? (int)((hi - lo - warp + NW - 1) / NW) : 0;
-    Cursor ci = cur;                                          // where the ring is filled
-    // chunk i: its descriptor {sequence, unit in the sequence, chunk, tokens of the sequence} and cache blocks
-    int4 dn = make_int4(0, 0, 0, 0);
+    // Where the ring is filled: chunk ck of unit u of sequence b, advanced by NW chunks at a time
+    // (no divisions in the loop); the chunk's cache blocks, looked up one chunk ahead of the copy
+    int ib, iu, ick, inck, ilen;
+    int64_t irow;                                             // block-table row of the unit's first block
+    {
+        Cursor ci = cur;
+        if (nmine > 0) cursor_to<CH>(a, units, lo + warp, ci);
+        const int64_t rel = lo + warp - ci.base;
+        ib = ci.b;
+        inck = ci.nck;
+        iu = (int)(rel / inck);
+        ick = (int)(rel - (int64_t)iu * inck);
+        ilen = (int)seq_len(a, ib);
+        irow = ((int64_t)ib * a.Hkv + iu / rgroups) * a.NB;
+    }
     int64_t kblk = 0, vblk = 0;
-    auto locate = [&](int i) {
-        const int64_t x = lo + warp + (int64_t)i * NW;
-        cursor_to<CH>(a, units, x, ci);
-        const int64_t rel = x - ci.base;
-        const int u = (int)(rel / ci.nck), ck = (int)(rel - (int64_t)u * ci.nck);
-        dn = make_int4(ci.b, u, ck, (int)seq_len(a, ci.b));
-        const int64_t bh = (int64_t)ci.b * a.Hkv + u / rgroups;
-        const int64_t lb = (int64_t)ck * CH >> 6;
-        if (dn.w == 0) {                                      // empty sequence: nothing to read
-            kblk = vblk = 0;
-            return;
+    auto locate = [&]() {
+        const int lb = (int)(((int64_t)ick * CH) >> 6);
+        kblk = vblk = 0;                                      // (an empty sequence reads block 0, all masked)
+        if (ilen > 0) {
+            kblk = table_entry(a.ktable, a.kpool, irow + lb, a.err);
+            vblk = table_entry(a.vtable, a.vpool, irow + lb, a.err);
         }
-        kblk = cache_block(a.ktable, a.kpool, a.NB, bh, lb, a.err);
-        vblk = cache_block(a.vtable, a.vpool, a.NB, bh, lb, a.err);
+    };
+    auto advance = [&]() {
+        ick += NW;
+        if (ick >= inck) {
+            do {
+                ick -= inck;
+                if (++iu == (int)units) {
+                    iu = 0;
+                    if (++ib == (int)a.B) { ib = 0; inck = NW; ick = 0; break; }        // behind the last chunk
+                    ilen = (int)seq_len(a, ib);
+                    inck = (int)seq_chunks<CH>(a, ib);
+                }
+            } while (ick >= inck);
+            irow = ((int64_t)ib * a.Hkv + iu / rgroups) * a.NB;
+        }
     };
     // lane k issues copy k of a stage: K codes, K pairs, V codes, V pairs
     int cp_off, cp_step, cp_dst, cp_size;
@@ -280,34 +310,52 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
         cp_size = cp_step = CH * (pairs ? S::kPairB : S::kCodeB);
         cp_dst = lane == 0 ? S::kOffKc : lane == 1 ? S::kOffKp : lane == 2 ? S::kOffVc : S::kOffVp;
     }
-    auto issue = [&](int i) {                                 // the chunk that locate(i) found
-        const int st = i % RING;
+    auto issue = [&](int st) {                                // the chunk that locate() found, into stage st
         const uint32_t br = smem_u32(&bar[st]);
         if (lane == 0) {
-            desc[st] = dn;
+            desc[st] = ick * CH;
             mbar_expect_tx(br, S::kStageB);
         }
         __syncwarp();
         if (lane < 4) {
             const int64_t blk = lane < 2 ? kblk : vblk;       // a bad table entry reads block 0
             const uint8_t* src = (lane < 2 ? a.kc : a.vc) + (blk >= 0 ? blk : 0) * S::kBlockB;
-            const int sub = (int)(((int64_t)dn.z * CH & 63) / CH);
+            const int sub = ((ick * CH) & 63) / CH;
             bulk_g2s(smem_u32(ring + st * S::kStageB + cp_dst), src + cp_off + sub * cp_step, (uint32_t)cp_size, br);
         }
     };
     // bytes that a kernel before this wrote (the encode) are read by bulk copies
     asm volatile("fence.proxy.async;" ::: "memory");
     for (int i = 0; i < RING && i < nmine; ++i) {
-        locate(i);
+        locate();
         issue(i);
+        advance();
     }
-    if (RING < nmine) locate(RING);
+    if (RING < nmine) locate();
+
+    // Lane constants: where this lane's codes sit in a tile (the swizzle repeats every 8 tokens),
+    // kept in registers for up to two groups; the order of its value tokens (2t, 2t + 1, the odd
+    // one first where t >= 2)
+    constexpr int kTileB = 16 * (D / 2);
+    constexpr int kKeep = NG <= 2 ? NG : 1;
+    const int par = tq4 >> 1, tv0 = 2 * tq4 + par, tv1 = 2 * tq4 + 1 - par;
+    const uint32_t sel_lo = par ? 0x1054u : 0x5410u, sel_hi = par ? 0x3276u : 0x7632u;
+    int kat[kKeep], vat0[kKeep], vat1[kKeep];
+#pragma unroll
+    for (int G_ = 0; G_ < kKeep; ++G_) {
+        kat[G_] = W::key_at(gr, G_, tq4);
+        vat0[G_] = W::value_at(tv0, G_, gr);
+        vat1[G_] = W::value_at(tv1, G_, gr);
+    }
+    auto at_k = [&](int gam) { return NG <= 2 ? kat[gam < kKeep ? gam : 0] : W::key_at(gr, gam, tq4); };
+    auto at_v0 = [&](int gam) { return NG <= 2 ? vat0[gam < kKeep ? gam : 0] : W::value_at(tv0, gam, gr); };
+    auto at_v1 = [&](int gam) { return NG <= 2 ? vat1[gam < kKeep ? gam : 0] : W::value_at(tv1, gam, gr); };
 
     // ---------------- units of this CTA, one after the other
     uint32_t bq[kFragSmem ? 1 : KNT][kFragSmem ? 1 : kKC][2];
     float o[NT][kKC][4], oz[NT][NG], mref[NT], lsum[NT], fq[NT], qs[NT][NG];
     bool live[NT];
-    int64_t lim[NT];                                          // tokens visible to this lane's rows
+    int lim[NT];                                              // tokens visible to this lane's rows
     bool failed = false;
     int i = 0;                                                // this warp's next chunk
     int stage = 0;
@@ -384,7 +432,6 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
 #pragma unroll
                 for (int kc = 0; kc < kKC; ++kc) frag(nt, kc, bq[nt][kc][0], bq[nt][kc][1]);
         }
-        int64_t minlim = len;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int h = 4 * nt + tq4;
@@ -396,13 +443,13 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
                 oz[nt][G_] = 0.f;
             }
             const int64_t l_ = len - a.Lq + 1 + (r0 + h) / a.G;
-            lim[nt] = live[nt] ? (l_ < 0 ? 0 : l_) : 0;
+            lim[nt] = live[nt] && l_ > 0 ? (int)l_ : 0;
             mref[nt] = -INFINITY;
             lsum[nt] = 0.f;
 #pragma unroll
             for (int mt = 0; mt < kKC; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
         }
-        minlim = len - a.Lq + 1 + r0 / a.G;                   // the unit's first row sees the fewest tokens
+        const int64_t minlim = len - a.Lq + 1 + r0 / a.G;     // the unit's first row sees the fewest tokens
 
         // ---------------- this warp's chunks of the unit
         for (; i < nmine && lo + warp + (int64_t)i * NW < x1 && !failed; ++i) {
@@ -416,7 +463,7 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
                 break;
             }
             const uint8_t* st = ring + stage * S::kStageB;
-            const int64_t tok0 = (int64_t)desc[stage].z * CH;
+            const int tok0 = desc[stage];
             auto tile = [&](const int kt, auto partial_tag) {
                 constexpr bool PARTIAL = decltype(partial_tag)::value;
                 const int tA = kt * 16 + gr, tB = tA + 8;     // this lane's two tokens
@@ -430,8 +477,8 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
 #pragma unroll
                 for (int gam = 0; gam < NG; ++gam) {
                     uint32_t wA[W::kK], wB[W::kK];
-                    W::key(st + S::kOffKc, tA, gam, tq4, wA);
-                    W::key(st + S::kOffKc, tB, gam, tq4, wB);
+                    W::key(st + kt * kTileB + S::kOffKc + at_k(gam), wA);
+                    W::key(st + kt * kTileB + S::kOffKc + at_k(gam) + 8 * (D / 2), wB);
                     float acc[KNT][4];
 #pragma unroll
                     for (int nt = 0; nt < KNT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
@@ -516,7 +563,6 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
                 // p (vz + 15 vs) - p vs (15 - c): codes are all positive and a long flat softmax
                 // would sum them to many times the result, with the tensor core's truncated
                 // additions (relative error against 64 bits at 4133 tokens 7e-5; this way 7e-7)
-                const int par = tq4 >> 1;
                 const float c15 = (gr & 1) ? 15.f : 0.f;      // this lane's tokens are odd
                 float qA[NT], qB[NT];
 #pragma unroll
@@ -524,8 +570,6 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
                     qA[nt] = (gr & 1) ? -pA[nt] : pA[nt];
                     qB[nt] = (gr & 1) ? -pB[nt] : pB[nt];
                 }
-                const uint32_t sel_lo = par ? 0x1054u : 0x5410u, sel_hi = par ? 0x3276u : 0x7632u;
-                const int v0 = kt * 16 + 2 * tq4 + par, v1 = kt * 16 + 2 * tq4 + 1 - par;
 #pragma unroll
                 for (int gam = 0; gam < NG; ++gam) {
                     uint32_t pb[NT][2];
@@ -545,21 +589,24 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
                         pb[nt][1] = movmatrix_t(__byte_perm(h, l, 0x7632));
                     }
                     uint32_t w0[W::kV], w1[W::kV], w2[W::kV], w3[W::kV];
-                    W::value(st + S::kOffVc, v0, gam, gr, w0);
-                    W::value(st + S::kOffVc, v1, gam, gr, w1);
-                    W::value(st + S::kOffVc, v0 + 8, gam, gr, w2);
-                    W::value(st + S::kOffVc, v1 + 8, gam, gr, w3);
+                    const uint8_t* vp = st + kt * kTileB + S::kOffVc;
+                    W::value(vp + at_v0(gam), w0);
+                    W::value(vp + at_v1(gam), w1);
+                    W::value(vp + at_v0(gam) + 8 * (D / 2), w2);
+                    W::value(vp + at_v1(gam) + 8 * (D / 2), w3);
 #pragma unroll
                     for (int k = 0; k < W::kV; ++k) {
 #pragma unroll
                         for (int half = 0; half < (GRP == 32 ? 1 : 2); ++half) {
                             // four values: the low halfword is token 2t's, the high one token 2t + 1's
                             const uint32_t sel = half ? sel_hi : sel_lo;
-                            const uint32_t x = __byte_perm(w0[k], w1[k], sel), y = __byte_perm(w2[k], w3[k], sel);
+                            // (its 15 - c)
+                            const uint32_t x = __byte_perm(w0[k], w1[k], sel) ^ 0xffff0000u;
+                            const uint32_t y = __byte_perm(w2[k], w3[k], sel) ^ 0xffff0000u;
                             const uint32_t x8 = x >> 8, y8 = y >> 8;
 #pragma unroll
                             for (int r = 0; r < 4; r += 2) {
-                                const uint32_t va[4] = {pick_odd(x, x8, r), pick_odd(x, x8, r + 1), pick_odd(y, y8, r), pick_odd(y, y8, r + 1)};
+                                const uint32_t va[4] = {pick(x, x8, r), pick(x, x8, r + 1), pick(y, y8, r), pick(y, y8, r + 1)};
                                 const int mt = gam * (GRP / 16) + k * 4 + half * 2 + (r >> 1);
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][mt], va, pb[nt][0], pb[nt][1]);
@@ -579,8 +626,9 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
             __syncwarp();
             if (i + RING < nmine) {
                 fence_proxy_async();
-                issue(i + RING);
-                if (i + RING + 1 < nmine) locate(i + RING + 1);
+                issue(stage);
+                advance();
+                if (i + RING + 1 < nmine) locate();
             }
             if (++stage == RING) { stage = 0; phase ^= 1; }
         }
