@@ -54,6 +54,8 @@ _lib = None
 def lib() -> C.CDLL:
     """Load the in-tree libtq.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
