@@ -65,9 +65,10 @@ __global__ void __launch_bounds__(256) tq_pages_fork_kernel(const PagesArgs a, c
     }
 }
 
-// ---------------------------------------------------------------- plans (one CTA)
+// ---------------------------------------------------------------- plans
 constexpr int kPlan = 1024;
-// exclusive scan of v over the CTA; *total: the sum
+// exclusive scan of v over the CTA of T threads; *total: the sum
+template <int T = kPlan>
 __device__ __forceinline__ int scan_cta(int v, int* total) {
     __shared__ int part[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -80,7 +81,7 @@ __device__ __forceinline__ int scan_cta(int v, int* total) {
     __syncthreads();                                   // part may still be read from an earlier scan
     if (lane == 31) part[warp] = incl;
     __syncthreads();
-    int p = part[lane];
+    int p = lane < T / 32 ? part[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(kFull, p, o);
@@ -90,28 +91,49 @@ __device__ __forceinline__ int scan_cta(int v, int* total) {
     const int before = warp ? __shfl_sync(kFull, p, warp - 1) : 0;
     return before + incl - v;
 }
-// Pages p of the warp's run of the pool, in order: f(p, refs, pages before p in the run that `pick` holds for)
-template <typename Pick, typename F>
-__device__ __forceinline__ int warp_run(const PagesArgs& a, Pick pick, F f) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t per = ((a.pool + 31) / 32 + 31) / 32 * 32;
-    const int64_t p0 = warp * per, p1 = p0 + per < a.pool ? p0 + per : a.pool;
-    int n = 0;
-    for (int64_t p = p0; p < p1; p += 32) {
-        const bool in = p + lane < p1;
-        const int r = in ? a.refs[p + lane] : 1;
-        const bool yes = in && pick(r);
-        const unsigned m = __ballot_sync(kFull, yes);
-        if (in) f(p + lane, r, yes, n + __popc(m & ((1u << lane) - 1u)));
-        n += __popc(m);
+// The pool in rounds of up to 64 pages per thread (65536 pages per round; thread t holds a run of
+// `per` pages, ascending in t): bit i of the mask says whether pick(refs) holds for page p0 + i.
+// One round's masks stay in registers, so a pool of that size is read once.
+struct Runs {
+    int64_t pool;
+    int per;          // pages per thread and round, a multiple of 4
+    int rounds;
+    bool vec;         // refs on a 16-byte boundary
+    __device__ explicit Runs(const PagesArgs& a) {
+        pool = a.pool;
+        const int64_t each = (pool + kPlan - 1) / kPlan;
+        per = each < 64 ? (int)((each + 3) / 4 * 4) : 64;
+        rounds = (int)((pool + (int64_t)per * kPlan - 1) / ((int64_t)per * kPlan));
+        vec = (reinterpret_cast<uintptr_t>(a.refs) & 15) == 0;
     }
-    return n;
-}
+    __device__ int64_t first(int round) const { return ((int64_t)round * kPlan + threadIdx.x) * per; }
+    template <typename Pick>
+    __device__ uint64_t mask(const PagesArgs& a, int round, Pick pick) const {
+        const int64_t p0 = first(round);
+        uint64_t m = 0;
+        if (vec && p0 + per <= pool) {
+#pragma unroll 4
+            for (int i = 0; i < per; i += 4) {
+                const int4 r = *reinterpret_cast<const int4*>(a.refs + p0 + i);
+                const uint32_t four = (uint32_t)pick(r.x) | (uint32_t)pick(r.y) << 1 | (uint32_t)pick(r.z) << 2 |
+                                      (uint32_t)pick(r.w) << 3;
+                m |= (uint64_t)four << i;
+            }
+        } else {
+            for (int i = 0; i < per; ++i)
+                if (p0 + i < pool && pick(a.refs[p0 + i])) m |= 1ull << i;
+        }
+        return m;
+    }
+};
 
 // Tokens [lo, hi) of every sequence become writable: each of their blocks that has no page,
 // or one that other entries name too, gets a fresh page.
 __global__ void __launch_bounds__(kPlan) tq_pages_alloc_kernel(const PagesArgs a, const int32_t* lo, const int32_t* hi,
                                                                int32_t* info) {
+    const Runs runs(a);
+    auto is_free = [](int r) { return r == 0; };
+    const uint64_t free0 = runs.mask(a, 0, is_free);
     const int64_t rows = a.B * a.Hkv, per = (rows + kPlan - 1) / kPlan;
     const int64_t r0 = threadIdx.x * per < rows ? threadIdx.x * per : rows, r1 = r0 + per < rows ? r0 + per : rows;
     // the requests of this thread's rows, in (row, block) order: f(table index, entry)
@@ -135,17 +157,29 @@ __global__ void __launch_bounds__(kPlan) tq_pages_alloc_kernel(const PagesArgs a
             }
         }
     };
-    int mine = 0, R, F;
-    requests([&](int64_t, int32_t) { ++mine; });
+    // (up to two requests are kept: a decode step asks for one block per row)
+    int mine = 0, R;
+    int64_t at0 = 0, at1 = 0;
+    int32_t e0 = 0, e1 = 0;
+    requests([&](int64_t at, int32_t e) {
+        if (mine == 0) { at0 = at; e0 = e; }
+        if (mine == 1) { at1 = at; e1 = e; }
+        ++mine;
+    });
     int rank = scan_cta(mine, &R);
-    const int nf = warp_run(a, [](int r) { return r == 0; }, [](int64_t, int, bool, int) {});
-    const int f0 = __shfl_sync(kFull, scan_cta((threadIdx.x & 31) == 0 ? nf : 0, &F), 0);
-    warp_run(a, [](int r) { return r == 0; },
-             [&](int64_t p, int, bool yes, int k) { if (yes && f0 + k < R) a.list[f0 + k] = (int32_t)p; });
+    // free pages, lowest first, as far as they are asked for
+    int F = 0;
+    for (int k = 0; k < runs.rounds; ++k) {
+        uint64_t m = k == 0 ? free0 : runs.mask(a, k, is_free);
+        int n;
+        int at = F + scan_cta(__popcll(m), &n);
+        for (; m && at < R; m &= m - 1, ++at) a.list[at] = (int32_t)(runs.first(k) + __ffsll((long long)m) - 1);
+        F += n;
+    }
     __syncthreads();
     const int got = R < F ? R : F;
     // (refs stay as they were until every request has been looked at again)
-    requests([&](int64_t at, int32_t e) {
+    auto give = [&](int64_t at, int32_t e) {
         if (rank < got) {
             const int32_t p = a.list[rank];
             a.from[rank] = e < 0 ? -1 : e;
@@ -153,7 +187,13 @@ __global__ void __launch_bounds__(kPlan) tq_pages_alloc_kernel(const PagesArgs a
             a.table[at] = p;
         }
         ++rank;
-    });
+    };
+    if (mine > 2) {
+        requests(give);
+    } else {
+        if (mine > 0) give(at0, e0);
+        if (mine > 1) give(at1, e1);
+    }
     __syncthreads();
     int zeroed = 0;
     for (int k = threadIdx.x; k < got; k += kPlan) {
@@ -171,34 +211,80 @@ __global__ void __launch_bounds__(kPlan) tq_pages_alloc_kernel(const PagesArgs a
     }
 }
 
-// The k-th lowest hole below the number of live pages takes the k-th highest live page.
-__global__ void __launch_bounds__(kPlan) tq_pages_compact_kernel(const PagesArgs a, int32_t* info) {
-    int L, n;
-    auto live = [](int r) { return r > 0; };
-    const int nl = warp_run(a, live, [](int64_t, int, bool, int) {});
-    const int l0 = __shfl_sync(kFull, scan_cta((threadIdx.x & 31) == 0 ? nl : 0, &L), 0);
-    int moves = 0;
-    warp_run(a, live, [&](int64_t p, int, bool yes, int k) {
-        const int before = l0 + k;                     // live pages below p
-        if (!yes && p < L) a.to[p - before] = (int32_t)p;
-        if (yes && p >= L) {
-            const int m = L - 1 - before;
-            a.from[m] = (int32_t)p;
-            a.rank[p] = m;
-            ++moves;
-        }
-    });
-    scan_cta(moves, &n);                               // (its barriers order the lists as well)
-    for (int k = threadIdx.x; k < n; k += kPlan) {
-        a.refs[a.to[k]] = a.refs[a.from[k]];
-        a.refs[a.from[k]] = 0;
+// Compaction: the k-th lowest hole below the number of live pages takes the k-th highest live page.
+// One CTA per segment of 2048 pages, 8 per thread: a first launch counts the live pages of every
+// segment, a second adds up the counts before its segment and lists holes and far pages (one CTA
+// alone took 24 to 36 us for 49152 pages; a single segment needs no first launch).  References and
+// table follow in the move kernel.
+constexpr int kSeg = 2048, kSegThreads = 256;
+// live bits of this thread's 8 pages from p0 on
+__device__ __forceinline__ uint32_t live8(const PagesArgs& a, int64_t p0) {
+    uint32_t m = 0;
+    if ((reinterpret_cast<uintptr_t>(a.refs) & 15) == 0 && p0 + 8 <= a.pool) {
+        const int4 x = *reinterpret_cast<const int4*>(a.refs + p0), y = *reinterpret_cast<const int4*>(a.refs + p0 + 4);
+        m = (uint32_t)(x.x > 0) | (uint32_t)(x.y > 0) << 1 | (uint32_t)(x.z > 0) << 2 | (uint32_t)(x.w > 0) << 3 |
+            (uint32_t)(y.x > 0) << 4 | (uint32_t)(y.y > 0) << 5 | (uint32_t)(y.z > 0) << 6 | (uint32_t)(y.w > 0) << 7;
+    } else {
+        for (int i = 0; i < 8; ++i)
+            if (p0 + i < a.pool && a.refs[p0 + i] > 0) m |= 1u << i;
     }
-    if (threadIdx.x == 0) {
-        a.counts[0] = n;
-        a.counts[1] = L;
+    return m;
+}
+__global__ void __launch_bounds__(kSegThreads) tq_pages_count_kernel(const PagesArgs a) {
+    pdl_trigger();
+    const int64_t p0 = (int64_t)blockIdx.x * kSeg + threadIdx.x * 8;
+    int n;
+    scan_cta<kSegThreads>(__popc(live8(a, p0)), &n);
+    if (threadIdx.x == 0) a.list[blockIdx.x] = n;
+}
+__global__ void __launch_bounds__(kSegThreads) tq_pages_compact_kernel(const PagesArgs a, int32_t* info) {
+    const int64_t s0 = (int64_t)blockIdx.x * kSeg, p0 = s0 + threadIdx.x * 8;
+    const uint32_t m = live8(a, p0);
+    int n;
+    const int mine = scan_cta<kSegThreads>(__popc(m), &n);
+    int64_t L = n, first = 0;                          // live pages in all, and before this segment
+    if (gridDim.x > 1) {
+        pdl_wait();
+        int all = 0, low = 0;
+        for (unsigned k = threadIdx.x; k < gridDim.x; k += kSegThreads) {
+            const int c = a.list[k];
+            all += c;
+            low += k < blockIdx.x ? c : 0;
+        }
+        int t;
+        scan_cta<kSegThreads>(all, &t);
+        L = t;
+        scan_cta<kSegThreads>(low, &t);
+        first = t;
+    }
+    int64_t before = first + mine;                     // live pages below p
+    int low = 0;                                       // live pages of this thread below L
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t p = p0 + i;
+        if ((m >> i) & 1u) {
+            if (p >= L) {
+                const int64_t to = L - 1 - before;
+                a.from[to] = (int32_t)p;
+                a.rank[p] = (int32_t)to;
+            } else {
+                ++low;
+            }
+            ++before;
+        } else if (p < L && p < a.pool) {
+            a.to[p - before] = (int32_t)p;
+        }
+    }
+    // the segment that holds page L (the last one where every page is live) knows the moves
+    int under;
+    scan_cta<kSegThreads>(low, &under);
+    if (threadIdx.x == 0 && ((s0 <= L && L < s0 + kSeg) || (L == a.pool && blockIdx.x == gridDim.x - 1 && L == s0 + kSeg))) {
+        const int32_t moves = (int32_t)(L - first - under);
+        a.counts[0] = moves;
+        a.counts[1] = (int32_t)L;
         if (info) {
             info[0] = (int32_t)(a.pool - L);
-            info[1] = n;
+            info[1] = moves;
         }
     }
 }
@@ -220,7 +306,8 @@ __device__ __forceinline__ void copy_page(const uint8_t* src, uint8_t* dst, uint
     }
 }
 
-// moves from[k] -> to[k], k < *count (or n where count is null); table: entries of moved pages follow (compact)
+// moves from[k] -> to[k], k < *count (or n where count is null); remap: references and table
+// entries of moved pages follow (compact)
 __global__ void __launch_bounds__(256) tq_pages_move_kernel(const PageBuffers b, const int32_t* from, const int32_t* to,
                                                             const int32_t* count, int64_t n, int64_t pool_src,
                                                             int64_t pool_dst, const PagesArgs a, int remap) {
@@ -242,6 +329,10 @@ __global__ void __launch_bounds__(256) tq_pages_move_kernel(const PageBuffers b,
         copy_page(b.src[q] + (int64_t)s * b.units[q] * 16, b.dst[q] + (int64_t)d * b.units[q] * 16, b.units[q]);
     }
     if (remap) {
+        for (int64_t k = blockIdx.x * 256ll + threadIdx.x; k < moves; k += gridDim.x * 256ll) {
+            a.refs[to[k]] = a.refs[from[k]];           // (a page moves once: sources and destinations are distinct)
+            a.refs[from[k]] = 0;
+        }
         const int32_t L = a.counts[1];
         const int64_t entries = a.B * a.Hkv * a.NB;
         for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < entries; i += gridDim.x * 256ll) {
@@ -274,20 +365,37 @@ cudaError_t launch_pages_fork(const PagesArgs& a, const int32_t* parent, cudaStr
     return cudaGetLastError();
 }
 
+// blocks of a move kernel whose number of moves only the device knows: enough for a warp per page
+// and buffer where there are few, four per SM at most
+static unsigned move_grid(const PagesArgs& a, const PageBuffers& b, int num_sms) {
+    const int64_t entries = a.B * a.Hkv * a.NB;
+    const int64_t pages = entries < a.pool ? entries : a.pool;
+    const int64_t need = (pages * (b.n > 0 ? b.n : 1) + 7) / 8, most = (int64_t)num_sms * 4;
+    return (unsigned)(need < 1 ? 1 : need < most ? need : most);
+}
+
 cudaError_t launch_pages_alloc(const PagesArgs& a, const PageBuffers& b, const int32_t* lo, const int32_t* hi, int32_t* info,
                                int num_sms, cudaStream_t s) {
     tq_pages_alloc_kernel<<<1, kPlan, 0, s>>>(a, lo, hi, info);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_pdl(tq_pages_move_kernel, dim3((unsigned)num_sms * 4), dim3(256), 0, s, b, (const int32_t*)a.from,
+    return launch_pdl(tq_pages_move_kernel, dim3(move_grid(a, b, num_sms)), dim3(256), 0, s, b, (const int32_t*)a.from,
                       (const int32_t*)a.to, (const int32_t*)a.counts, (int64_t)0, a.pool, a.pool, a, 0);
 }
 
 cudaError_t launch_pages_compact(const PagesArgs& a, const PageBuffers& b, int32_t* info, int num_sms, cudaStream_t s) {
-    tq_pages_compact_kernel<<<1, kPlan, 0, s>>>(a, info);
-    cudaError_t e = cudaGetLastError();
+    const unsigned segments = (unsigned)((a.pool + kSeg - 1) / kSeg);
+    cudaError_t e = cudaSuccess;
+    if (segments > 1) {
+        tq_pages_count_kernel<<<segments, kSegThreads, 0, s>>>(a);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) e = launch_pdl(tq_pages_compact_kernel, dim3(segments), dim3(kSegThreads), 0, s, a, info);
+    } else {
+        tq_pages_compact_kernel<<<1, kSegThreads, 0, s>>>(a, info);
+        e = cudaGetLastError();
+    }
     if (e != cudaSuccess) return e;
-    return launch_pdl(tq_pages_move_kernel, dim3((unsigned)num_sms * 4), dim3(256), 0, s, b, (const int32_t*)a.from,
+    return launch_pdl(tq_pages_move_kernel, dim3(move_grid(a, b, num_sms)), dim3(256), 0, s, b, (const int32_t*)a.from,
                       (const int32_t*)a.to, (const int32_t*)a.counts, (int64_t)0, a.pool, a.pool, a, 1);
 }
 

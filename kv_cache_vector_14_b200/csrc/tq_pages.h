@@ -23,7 +23,7 @@ struct PagesArgs {
     int32_t* from;            // [pool] moves: source page (alloc: -1 where nothing is copied)
     int32_t* to;              // [pool] destination page
     int32_t* rank;            // [pool] compact: move that takes a page away
-    int32_t* list;            // [pool] alloc: free pages, lowest first
+    int32_t* list;            // [pool] alloc: free pages, lowest first; compact: live pages per segment
 };
 struct PagesWs {
     size_t off_from, off_to, off_rank, off_list, bytes;

@@ -151,21 +151,35 @@ def _np_ptr(a: np.ndarray):
     return a.ctypes.data_as(C.c_void_p)
 
 
+_raw_stream = _device = None     # torch's accessors of the current stream and device, and its dtypes,
+_codes = {}                      # looked up once: a call of the small operators costs the host a few microseconds
+
+
+def _torch_accessors():
+    global _raw_stream, _device
+    import torch
+    _codes.update({torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16})
+    _device = torch._C._cuda_getDevice
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return C.c_void_p(torch.cuda.current_stream().cuda_stream)
+        if _raw_stream is None:
+            _torch_accessors()
+        return _raw_stream(_device())
     if isinstance(stream, int):
-        return C.c_void_p(stream)
-    return C.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 def _dtype_code(t) -> int:
-    import torch
-    m = {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}
-    if t.dtype not in m:
+    if not _codes:
+        _torch_accessors()
+    code = _codes.get(t.dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
-    return m[t.dtype]
+    return code
 
 
 # ------------------------------------------------------------------ constants
@@ -372,37 +386,37 @@ def _int32(t, name: str, n: int):
     """Pointer of a device int32 vector of n elements (None stays None)."""
     if t is None:
         return None
-    import torch
-    if t.dtype is not torch.int32 or t.numel() != n or not t.is_contiguous():
+    if str(t.dtype) != "torch.int32" or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous int32 with {n} elements")
     return t.data_ptr()
 
 
-def _same_group(name: str, h, *caches):
+def _same_group(name: str, h, a, b):
     d = lib().tq_head_dim(h)
-    if any(c.head_dim != d or c.group != caches[0].group for c in caches):
+    if a.head_dim != d or b.head_dim != d or a.group != b.group:
         raise ValueError(f"{name}: the caches need the handle's head_dim and one group")
     return d
 
 
-def _int4_copy(name, h, x, cache: Int4Cache, t0: int, pos, stream):
-    d = _same_group(name, h, cache)
-    if x.dim() != 4 or x.shape[3] != d or x.stride(3) != 1:
+def _int4_copy(fn, name, h, x, cache: Int4Cache, t0: int, pos, stream):
+    d = _same_group(name, h, cache, cache)
+    shape, strides = x.shape, x.stride()
+    if len(shape) != 4 or shape[3] != d or strides[3] != 1:
         raise ValueError(f"{name}: the vectors must be [B, Hkv, T, {d}] with a contiguous last dim")
-    B, Hkv, T, _ = x.shape
-    sb, sh, st_, _ = x.stride()
-    _check(getattr(lib(), name)(h, cache.group, x.data_ptr(), _dtype_code(x), B, Hkv, T, sb, sh, st_, cache._ref,
-                                _int32(pos, "pos", B), t0, _stream(stream)), name)
+    B, Hkv, T, _ = shape
+    sb, sh, st_, _ = strides
+    _check(fn(h, cache.group, x.data_ptr(), _dtype_code(x), B, Hkv, T, sb, sh, st_, cache._ref,
+              _int32(pos, "pos", B), t0, _stream(stream)), name)
 
 
 def tq_encode_int4(h, x, cache: Int4Cache, t0: int = 0, pos=None, stream=None) -> None:
     """Encode x [B, Hkv, T, d] at positions pos[b] + i (pos: int32 [B]) or t0 + i."""
-    _int4_copy("tq_encode_int4", h, x, cache, t0, pos, stream)
+    _int4_copy(lib().tq_encode_int4, "tq_encode_int4", h, x, cache, t0, pos, stream)
 
 
 def tq_expand_int4(h, cache: Int4Cache, out, t0: int = 0, pos=None, stream=None) -> None:
     """Read out.shape[2] tokens back into out [B, Hkv, T, d] from positions pos[b] + i or t0 + i."""
-    _int4_copy("tq_expand_int4", h, out, cache, t0, pos, stream)
+    _int4_copy(lib().tq_expand_int4, "tq_expand_int4", h, out, cache, t0, pos, stream)
 
 
 def tq_attend_int4_workspace_bytes(h, B: int, Lq: int, Hq: int, Hkv: int) -> int:
@@ -410,11 +424,12 @@ def tq_attend_int4_workspace_bytes(h, B: int, Lq: int, Hq: int, Hkv: int) -> int
 
 
 def _int4_queries(name, d, q, out):
-    if q.dim() not in (3, 4) or q.shape[-1] != d or not q.is_contiguous():
+    shape = q.shape
+    if len(shape) not in (3, 4) or shape[-1] != d or not q.is_contiguous():
         raise ValueError(f"{name}: q must be contiguous [B, Lq, Hq, {d}] (or [B, Hq, {d}])")
-    if out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+    if out.shape != shape or out.dtype != q.dtype or not out.is_contiguous():
         raise ValueError(f"{name}: out must be contiguous with q's shape and dtype")
-    return q.shape[0], (q.shape[1] if q.dim() == 4 else 1), q.shape[-2]
+    return shape[0], (shape[1] if len(shape) == 4 else 1), shape[-2]
 
 
 def tq_attend_int4(h, q, kc: Int4Cache, vc: Int4Cache, out, ws, T: int = 0, seq_lens=None, scale: float = 1.0,
@@ -488,7 +503,7 @@ def tq_pages_alloc(h, pages: Pages, lo, hi, info, ws, stream=None) -> None:
     """Make tokens [lo[b], hi[b]) writable: missing pages are supplied, shared ones
     copied.  info (int32 [2] or None): free pages left, blocks left without."""
     _check(lib().tq_pages_alloc(h, pages._ref, _int32(lo, "lo", pages.B), _int32(hi, "hi", pages.B),
-                                _int32(info, "info", 2), ws.data_ptr(), ws.numel() * ws.element_size(),
+                                _int32(info, "info", 2), ws.data_ptr(), ws.nbytes,
                                 _stream(stream)), "tq_pages_alloc")
 
 

@@ -213,7 +213,7 @@ def test_free(libtq, keep):
 
 @gpu
 @pytest.mark.parametrize("pool,lens", [(40, [300, 300, 0]), (45, [300, 300, 300]), (1000, [320, 1, 70]), (33000, [320, 320, 5]),
-                                       (64, [0, 0, 0])])
+                                       (64, [0, 0, 0]), (150001, [320, 320, 300])])
 @pytest.mark.parametrize("sizes", [(160, 48), (4608, 4608, 16, 6144), ()])
 def test_compact(libtq, pool, lens, sizes):
     table, refs, pools = build(3, 2, 5, pool, lens, seed=pool, share=2, sizes=sizes)
