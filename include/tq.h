@@ -348,8 +348,12 @@ TQ_API size_t tq_attend_int4_workspace_bytes(const tq_handle* h, int64_t B, int6
  * uses kv head h / (Hq/Hkv); scores are scale <q, k>, softmax and sums in fp32.
  * What lies in the caches behind a query's last visible token has no effect on
  * it, whatever it is.  Sequences may have any mixture of lengths: the work is
- * shared out over the SMs on the device.  fp32 queries are taken to 22 bits
- * relative to their row's largest element, 16-bit queries exactly.
+ * shared out over the SMs on the device.  Precision: sums, maxima and softmax
+ * statistics are fp32 (integer products exact); queries, keys, weights and
+ * values carry at least 22 bits for fp32 and fp16 calls.  bf16 calls round the
+ * weights times the value scales to fp16 (2^-11, against 2^-8 of their output),
+ * and with more than 8 query rows per kv head (head_dim 64 and 128) the
+ * expanded keys and values too.
  * Supported: any Hq/Hkv, B < 2^31, Lq * Hq / Hkv < 2^31, Hkv * row groups <
  * 2^31 (row groups: query rows per kv head / 4, rounded up); contiguous or
  * paged caches.  ws: 256-byte aligned, at least

@@ -6,17 +6,25 @@
 //   s_t = scale sum_G (ks_{t,G} sum_{j in G} q_j c_{t,j} + kz_{t,G} sum_{j in G} q_j)
 //   out = sum_t p_t (vz_{t,G} + vs_{t,G} cv_{t,j}) / sum_t p_t,   p_t = 2^(s_t log2 e - m)
 //
-// Operands.  A nibble c placed in the low mantissa bits of an fp16 is the
-// subnormal number c 2^-24 (16 c 2^-24 one nibble higher), which the tensor
-// core multiplies exactly, so a code costs one AND per pair and one shift per
-// four pairs, no conversion.  The factors 2^24 and 16 go into the query
-// (power-of-two scaled per row), and into the result.  q enters as fp16 hi and
-// lo limbs (22 bits; 16-bit queries need only hi), the softmax weights times
-// the value scales, p vs, as hi and lo limbs in the columns of one operand.
+// Operands.  What bounds the kernel is the integer pipe that takes codes apart, so
+// the operands are chosen for few instructions per code:
+//   * Keys enter as int8 operands without being unpacked.  A byte is c0 + 16 c1, so
+//     q0 c0 + q1 c1 = (q1 / 16) byte + (q0 - q1 / 16) (byte & 15): the stored words
+//     and the words with the high nibbles masked off are the two halves of a k = 32
+//     step, one AND per eight codes.  The queries are 32-bit fixed point relative to
+//     the row's largest element, in four signed byte limbs; a lane's columns are the
+//     limbs of its own head.
+//   * A value nibble c in the low mantissa bits of an fp16 is the subnormal number
+//     c 2^-24 (16 c 2^-24 one nibble higher), which the tensor core multiplies
+//     exactly: one AND per pair and one shift per four pairs, no conversion.  A
+//     transposing shared-memory load brings the nibbles of two tokens into one
+//     register.  The softmax weights times the value scales, p vs, are the other
+//     operand: fp16 hi and lo limbs in two columns (22 bits), for bf16 outputs hi
+//     alone (2^-11 relative, against 2^-8 of the output's rounding).
 // The products with the zeros are rank-one: fp32 sums outside the tensor core.
 // To keep p vs inside fp16 whatever the values' magnitude, the reference
 // exponent m follows the maximum of s_t + log2 max_G vs_{t,G} rather than of s_t.
-//   scores  S[16 tok][8] += C[16 tok][16 values] Q[16 values][8]     (group/16 steps per group)
+//   scores  S[16 tok][8] += C[16 tok][32] Q[32][8]                   (int8, group/32 steps per group)
 //   values  O^T[16 values][8] += Cv^T[16 values][16 tok] P[16 tok][8], one P per group
 // Lane (g, t) = (lane / 4, lane % 4) owns tokens g and g + 8 of a 16-token tile
 // and head t (and 4 + t with two n-tiles).
@@ -56,11 +64,12 @@ struct Shape {
     static constexpr int kStageB = kOffVp + kChunk * kPairB;
     static constexpr int kBlockB = kBlockT * (kCodeB + kPairB);
     static constexpr int kRows = 4 * NT;                      // query rows of a unit
+    static constexpr int kTogether = kTiles;                  // tiles worked on at once
     // shared memory
     static constexpr int kOffAcc = kNW * kRing * kStageB;                 // [NW][kRows][D] merge buffers
     static constexpr int kOffQ = kOffAcc + kNW * kRows * D * 4;           // [kRows][D] scaled queries
-    static constexpr int kOffFrag = kOffQ + kRows * D * 4;                // D = 256: query fragments [NT][16][32]
-    static constexpr int kOffQs = kOffFrag + (D == 256 ? NT * (D / 16) * 32 * 8 : 0);   // [kRows][kNG]
+    static constexpr int kOffFrag = kOffQ + kRows * D * 4;                // D = 256: query fragments [2 NT][D / 32][32]
+    static constexpr int kOffQs = kOffFrag + (D == 256 ? 2 * NT * (D / 32) * 32 * 8 : 0);   // [kRows][kNG]
     static constexpr int kOffF = kOffQs + kRows * kNG * 4;                // [kRows]
     static constexpr int kOffMl = kOffF + kRows * 4;                      // [NW][kRows][2]
     static constexpr int kOffDesc = kOffMl + kNW * kRows * 8;             // [NW][kRing] int
@@ -73,6 +82,7 @@ struct Shape {
 };
 
 constexpr float kTwo24 = 16777216.f;
+constexpr float kHuge = 3.4e38f;
 constexpr float kRoom = 7.f;      // p vs is kept below 2^(kRoom + kLazy) = 2^15 (fp16 holds 65504) ...
 constexpr float kLazy = 8.f;      // ... and the reference exponent moves only when it is exceeded by this much
 
@@ -139,24 +149,39 @@ struct Words {
             w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
         }
     }
-    // V: the GRP / 8 values of group gam that lane row g holds of token tok: 1 or 2 words, or a halfword
-    static constexpr int kV = GRP == 128 ? 2 : 1;
-    static __device__ __forceinline__ int value_at(int tok, int gam, int g) {
-        return tok * (D / 2) + ((gam * (GRP / 2) + g * (GRP / 16)) ^ int4_swizzle(D, tok));
-    }
-    static __device__ __forceinline__ void value(const uint8_t* p, uint32_t (&w)[kV]) {
-        if constexpr (GRP == 32) w[0] = *reinterpret_cast<const uint16_t*>(p);
-        else if constexpr (GRP == 64) w[0] = *reinterpret_cast<const uint32_t*>(p);
-        else {
-            const uint2 v = *reinterpret_cast<const uint2*>(p);
-            w[0] = v.x; w[1] = v.y;
-        }
-    }
 };
-// nibbles r (and r + 4) of a word as two fp16 subnormals: c 2^-24 for even r, 16 c 2^-24 for odd
-__device__ __forceinline__ uint32_t pick(uint32_t w, uint32_t w8, int r) {
-    return (r < 2 ? w : w8) & ((r & 1) ? 0x00f000f0u : 0x000f000fu);
+// four 8 x 8 matrices of 16-bit elements, transposed: element rows 2t, 2t + 1 of column g each
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
 }
+// D += A B, A unsigned and B signed 8-bit, exact 32-bit accumulation
+__device__ __forceinline__ void imma_u8s8(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// nibble R of both halves of x as fp16 subnormals (c 2^-24 for even R, 16 c 2^-24 for odd), the
+// high half's as 15 - c: (x & mask) ^ flip in one instruction; x8 = x >> 8
+template <int R>
+__device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t x8) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;"
+        : "=r"(r)
+        : "r"(R < 2 ? x : x8), "r"((R & 1) ? 0x00f000f0u : 0x000f000fu), "r"((R & 1) ? 0x00f00000u : 0x000f0000u));
+    return r;
+}
+// v as four signed byte digits, v = l0 + 256 l1 + 65536 l2 + 2^24 l3 (adding 128 to each of the
+// lower bytes carries, the exclusive or takes it off again), and byte l of four words as one
+__device__ __forceinline__ uint32_t digits(int v) { return ((uint32_t)v + 0x00808080u) ^ 0x00808080u; }
+__device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d, int l) {
+    const uint32_t sel = (uint32_t)(l | ((4 + l) << 4));
+    return __byte_perm(__byte_perm(a, b, sel), __byte_perm(c, d, sel), 0x5410);
+}
+
 // pool block of a block-table entry (contiguous cache: the row itself); bad: -1 and the check word
 __device__ __forceinline__ int64_t table_entry(const int32_t* table, int64_t pool, int64_t row, int* err) {
     if (!table) return row;
@@ -173,14 +198,15 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
     using S = Shape<D, GRP, NT>;
     using W = Words<D, GRP>;
     constexpr int NG = S::kNG, NW = S::kNW, CH = S::kChunk, ROWS = S::kRows, RING = S::kRing;
-    constexpr int kKC = D / 16;                               // k-steps of a score
-    // K n-tiles: with one (NT = 1, or 16-bit queries) the columns are (head, limb) or (head t, head 4 + t)
-    constexpr int KNT = (NT == 2 && DT == TQ_F32) ? 2 : 1;
-    constexpr bool kTwoHeads = NT == 2 && KNT == 1;
+    constexpr int kWords = D / 32;                            // key words per lane and token: k-steps of a score
+    constexpr int kMT = D / 16;                               // 16-value tiles of the output
+    // bf16 outputs: weights as one fp16 limb, columns (head t, head 4 + t); else (hi, lo) of head t per n-tile
+    constexpr bool kOneLimb = DT == TQ_BF16;
+    constexpr int VT = kOneLimb ? 1 : NT;                     // value n-tiles
     constexpr bool kFragSmem = D == 256;
     extern __shared__ __align__(128) uint8_t smem[];
     float* sAcc = reinterpret_cast<float*>(smem + S::kOffAcc);
-    float* sQ = reinterpret_cast<float*>(smem + S::kOffQ);
+    uint32_t* sQ = reinterpret_cast<uint32_t*>(smem + S::kOffQ);
     [[maybe_unused]] uint2* sFrag = reinterpret_cast<uint2*>(smem + S::kOffFrag);
     float* sQs = reinterpret_cast<float*>(smem + S::kOffQs);
     float* sF = reinterpret_cast<float*>(smem + S::kOffF);
@@ -333,28 +359,24 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
     }
     if (RING < nmine) locate();
 
-    // Lane constants: where this lane's codes sit in a tile (the swizzle repeats every 8 tokens),
-    // kept in registers for up to two groups; the order of its value tokens (2t, 2t + 1, the odd
-    // one first where t >= 2)
+    // Lane constants: where this lane's key words and value rows sit in a tile (the swizzle repeats
+    // every 8 tokens), kept in registers for up to two groups (two 64-value pieces)
     constexpr int kTileB = 16 * (D / 2);
-    constexpr int kKeep = NG <= 2 ? NG : 1;
-    const int par = tq4 >> 1, tv0 = 2 * tq4 + par, tv1 = 2 * tq4 + 1 - par;
-    const uint32_t sel_lo = par ? 0x1054u : 0x5410u, sel_hi = par ? 0x3276u : 0x7632u;
-    int kat[kKeep], vat0[kKeep], vat1[kKeep];
+    constexpr int kKeepK = NG <= 2 ? NG : 1, kKeepV = D <= 128 ? D / 64 : 1;
+    // value loads: lane l gives row l % 8 of matrix l / 8: tokens 0-7 and 8-15 of one 16-byte piece, then of the next
+    const int vtok = 8 * ((lane >> 3) & 1) + (lane & 7), vbase = vtok * (D / 2) + 16 * (lane >> 4);
+    int kat[kKeepK], vat[kKeepV];
 #pragma unroll
-    for (int G_ = 0; G_ < kKeep; ++G_) {
-        kat[G_] = W::key_at(gr, G_, tq4);
-        vat0[G_] = W::value_at(tv0, G_, gr);
-        vat1[G_] = W::value_at(tv1, G_, gr);
-    }
-    auto at_k = [&](int gam) { return NG <= 2 ? kat[gam < kKeep ? gam : 0] : W::key_at(gr, gam, tq4); };
-    auto at_v0 = [&](int gam) { return NG <= 2 ? vat0[gam < kKeep ? gam : 0] : W::value_at(tv0, gam, gr); };
-    auto at_v1 = [&](int gam) { return NG <= 2 ? vat1[gam < kKeep ? gam : 0] : W::value_at(tv1, gam, gr); };
+    for (int G_ = 0; G_ < kKeepK; ++G_) kat[G_] = W::key_at(gr, G_, tq4);
+#pragma unroll
+    for (int c2 = 0; c2 < kKeepV; ++c2) vat[c2] = vbase + ((32 * c2) ^ int4_swizzle(D, vtok));
+    auto at_k = [&](int gam) { return NG <= 2 ? kat[gam < kKeepK ? gam : 0] : W::key_at(gr, gam, tq4); };
+    auto at_v = [&](int c2) { return D <= 128 ? vat[c2 < kKeepV ? c2 : 0] : vbase + ((32 * c2) ^ int4_swizzle(D, vtok)); };
+    const float c15 = (gr & 1) ? 15.f : 0.f, odd = (gr & 1) ? -1.f : 1.f;     // this lane's tokens are odd ones
 
     // ---------------- units of this CTA, one after the other
-    uint32_t bq[kFragSmem ? 1 : KNT][kFragSmem ? 1 : kKC][2];
-    float o[NT][kKC][4], oz[NT][NG], mref[NT], lsum[NT], fq[NT], qs[NT][NG];
-    bool live[NT];
+    uint32_t bq[kFragSmem ? 1 : 2 * NT][kFragSmem ? 1 : kWords][2];
+    float o[VT][kMT][4], oz[NT][NG], mref[NT], mexp[NT], lsum[NT], fq[NT], qs[NT][NG];
     int lim[NT];                                              // tokens visible to this lane's rows
     bool failed = false;
     int i = 0;                                                // this warp's next chunk
@@ -374,26 +396,32 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
             const int64_t qi = (r0 + r) / a.G, g = (r0 + r) - qi * a.G;
             return ((int64_t)cur.b * a.Lq + qi) * a.Hq + (int64_t)kv * a.G + g;
         };
-        // queries: row r scaled by a power of two so that its largest element is in [2^14, 2^15)
+        // queries: row r in fixed point, scaled by a power of two so that its largest element is in
+        // [2^28, 2^29); an even value's entry is q0 - q1 / 16, an odd one's q1 / 16
         for (int r = warp; r < ROWS; r += NW) {
             float v[D / 32], mx = 0.f;
+            bool bad = false;
             const int64_t at = (r < nrow ? out_row(r) : 0) * D;
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) {
                 v[e] = r < nrow ? load_elem<DT>(a.q, at + 32 * e + lane) : 0.f;
                 mx = fmaxf(mx, fabsf(v[e]));
+                bad |= !(fabsf(v[e]) <= kHuge);
             }
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, s));
-            int ex = mx > 0.f ? ilogbf(mx) : 0;
-            ex = ex < -100 ? -100 : ex;
-            const float f = mx <= 3.4e38f ? exp2f((float)(14 - ex)) : 1.f;
+            bad = __any_sync(kFull, bad);                     // an infinity or a NaN makes the row NaN
+            int ex = mx > 0.f && !bad ? ilogbf(mx) : 0;
+            ex = ex < -90 ? -90 : ex;
+            const float f = exp2f((float)(28 - ex));
             float gs[NG];
 #pragma unroll
             for (int G_ = 0; G_ < NG; ++G_) gs[G_] = 0.f;
 #pragma unroll
             for (int e = 0; e < D / 32; ++e) {
-                sQ[r * D + 32 * e + lane] = v[e] * f;
+                const int fix = __float2int_rn(v[e] * f * ((lane & 1) ? 0.0625f : 1.f));
+                const int high = __shfl_xor_sync(kFull, fix, 1);
+                sQ[r * D + 32 * e + lane] = digits((lane & 1) ? fix : fix - high);
                 gs[e / (GRP / 32)] += v[e];
             }
 #pragma unroll
@@ -402,40 +430,48 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
                 for (int s = 16; s > 0; s >>= 1) gs[G_] += __shfl_xor_sync(kFull, gs[G_], s);
                 if (lane == 0) sQs[r * NG + G_] = a.scale_log2 * gs[G_];
             }
-            if (lane == 0) sF[r] = a.scale_log2 * (kTwo24 / f);
+            if (lane == 0) sF[r] = bad ? __int_as_float(0x7fc00000) : a.scale_log2 / f;
         }
         __syncthreads();
-        // B operand of k-step kc: step (group, word j, half hf) covers, for lane quarter t, values
-        // 8 w + r and 8 w + r + 4, r = 2 hf (rows 2t, 2t + 1) and 2 hf + 1 (rows 2t + 8, + 9, scaled by 1/16)
-        auto frag = [&](int nt, int kc, uint32_t& b0, uint32_t& b1) {
-            const int gam = kc / (GRP / 16), in = kc % (GRP / 16), j = in >> 1, hf = in & 1;
+        // B operand of k-step (group, word j), n-tile (nt, p): column n is head 4 nt + n / 2, limb
+        // 2 p + n % 2, so that this lane's own columns are limbs 2 p, 2 p + 1 of head 4 nt + t.  Rows
+        // 4 t + e belong to byte e of lane quarter t's word, rows 16 + 4 t + e to its low nibbles.
+        auto frag = [&](int nt, int kw, uint2 (&b)[2]) {      // both n-tiles p of heads 4 nt ..
+            const int gam = kw / (GRP / 32), j = kw % (GRP / 32);
             const int w = gam * (GRP / 8) + tq4 * (GRP / 32) + j;
-            const int head = kTwoHeads ? (gr >> 1) + 4 * (gr & 1) : 4 * nt + (gr >> 1);
-            const float* p = sQ + head * D + 8 * w + 2 * hf;
-            uint32_t h0, l0, h1, l1;
-            split_hilo(p[0], p[4], h0, l0);
-            split_hilo(p[1] * 0.0625f, p[5] * 0.0625f, h1, l1);
-            const bool lolimb = !kTwoHeads && (gr & 1);
-            b0 = lolimb ? l0 : h0;
-            b1 = lolimb ? l1 : h1;
+            const uint4* p = reinterpret_cast<const uint4*>(sQ + (4 * nt + (gr >> 1)) * D + 8 * w);
+            const uint4 x = p[0], y = p[1];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int l = 2 * q + (gr & 1);
+                b[q] = make_uint2(bytes4(x.y, x.w, y.y, y.w, l), bytes4(x.x, x.z, y.x, y.z, l));
+            }
         };
         if constexpr (kFragSmem) {
-            for (int idx = warp; idx < KNT * kKC; idx += NW) {
-                uint32_t b0, b1;
-                frag(idx / kKC, idx % kKC, b0, b1);
-                sFrag[idx * 32 + lane] = make_uint2(b0, b1);
+            for (int idx = warp; idx < NT * kWords; idx += NW) {
+                uint2 b[2];
+                frag(idx / kWords, idx % kWords, b);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) sFrag[((2 * (idx / kWords) + q) * kWords + idx % kWords) * 32 + lane] = b[q];
             }
             __syncthreads();
         } else {
 #pragma unroll
-            for (int nt = 0; nt < KNT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int kc = 0; kc < kKC; ++kc) frag(nt, kc, bq[nt][kc][0], bq[nt][kc][1]);
+                for (int kw = 0; kw < kWords; ++kw) {
+                    uint2 b[2];
+                    frag(nt, kw, b);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        bq[2 * nt + q][kw][0] = b[q].x;
+                        bq[2 * nt + q][kw][1] = b[q].y;
+                    }
+                }
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int h = 4 * nt + tq4;
-            live[nt] = h < nrow;
             fq[nt] = sF[h];
 #pragma unroll
             for (int G_ = 0; G_ < NG; ++G_) {
@@ -443,12 +479,15 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
                 oz[nt][G_] = 0.f;
             }
             const int64_t l_ = len - a.Lq + 1 + (r0 + h) / a.G;
-            lim[nt] = live[nt] && l_ > 0 ? (int)l_ : 0;
+            lim[nt] = h < nrow && l_ > 0 ? (int)l_ : 0;
             mref[nt] = -INFINITY;
+            mexp[nt] = 0.f;                                   // the reference used in exponents (0 before any token)
             lsum[nt] = 0.f;
-#pragma unroll
-            for (int mt = 0; mt < kKC; ++mt) o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
         }
+#pragma unroll
+        for (int vt = 0; vt < VT; ++vt)
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt) o[vt][mt][0] = o[vt][mt][1] = o[vt][mt][2] = o[vt][mt][3] = 0.f;
         const int64_t minlim = len - a.Lq + 1 + r0 / a.G;     // the unit's first row sees the fewest tokens
 
         // ---------------- this warp's chunks of the unit
@@ -464,80 +503,91 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
             }
             const uint8_t* st = ring + stage * S::kStageB;
             const int tok0 = desc[stage];
-            auto tile = [&](const int kt, auto partial_tag) {
+            // NTILE 16-token tiles from tile k0 on, together: more independent work per warp, and one
+            // maximum exchange for all of them
+            auto tiles = [&](auto ntile_tag, const int k0, auto partial_tag) {
                 constexpr bool PARTIAL = decltype(partial_tag)::value;
-                const int tA = kt * 16 + gr, tB = tA + 8;     // this lane's two tokens
+                constexpr int NTILE = decltype(ntile_tag)::value;
+                constexpr int NP = 2 * NTILE;                 // this lane's tokens: g and g + 8 of every tile
                 // ---- scores
-                float s0[NT], s1[NT];
+                float sc[NT][NP], zc[NT][NP];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) s0[nt] = s1[nt] = 0.f;
-                float z0[NT], z1[NT];
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) z0[nt] = z1[nt] = 0.f;
+                    for (int k = 0; k < NP; ++k) sc[nt][k] = zc[nt][k] = 0.f;
 #pragma unroll
-                for (int gam = 0; gam < NG; ++gam) {
-                    uint32_t wA[W::kK], wB[W::kK];
-                    W::key(st + kt * kTileB + S::kOffKc + at_k(gam), wA);
-                    W::key(st + kt * kTileB + S::kOffKc + at_k(gam) + 8 * (D / 2), wB);
-                    float acc[KNT][4];
+                for (int kt = 0; kt < NTILE; ++kt) {
+                    const uint8_t* kc = st + (k0 + kt) * kTileB + S::kOffKc;
+                    const uint8_t* kp = st + S::kOffKp + ((k0 + kt) * 16 + gr) * S::kPairB;
 #pragma unroll
-                    for (int nt = 0; nt < KNT; ++nt) acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+                    for (int gam = 0; gam < NG; ++gam) {
+                        uint32_t wA[W::kK], wB[W::kK];
+                        W::key(kc + at_k(gam), wA);
+                        W::key(kc + at_k(gam) + 8 * (D / 2), wB);
+                        int acc[2 * NT][4];
 #pragma unroll
-                    for (int j = 0; j < W::kK; ++j) {
-                        const uint32_t wA8 = wA[j] >> 8, wB8 = wB[j] >> 8;
+                        for (int np = 0; np < 2 * NT; ++np) acc[np][0] = acc[np][1] = acc[np][2] = acc[np][3] = 0;
 #pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            const uint32_t ka[4] = {pick(wA[j], wA8, 2 * hf), pick(wB[j], wB8, 2 * hf),
-                                                    pick(wA[j], wA8, 2 * hf + 1), pick(wB[j], wB8, 2 * hf + 1)};
-                            const int kc = gam * (GRP / 16) + 2 * j + hf;
+                        for (int j = 0; j < W::kK; ++j) {
+                            const uint32_t ka[4] = {wA[j], wB[j], wA[j] & 0x0f0f0f0fu, wB[j] & 0x0f0f0f0fu};
+                            const int kw = gam * (GRP / 32) + j;
 #pragma unroll
-                            for (int nt = 0; nt < KNT; ++nt) {
+                            for (int np = 0; np < 2 * NT; ++np) {
                                 if constexpr (kFragSmem) {
-                                    const uint2 b = sFrag[(nt * kKC + kc) * 32 + lane];
-                                    mma16816(acc[nt], ka, b.x, b.y);
+                                    const uint2 b = sFrag[(np * kWords + kw) * 32 + lane];
+                                    imma_u8s8(acc[np], ka, b.x, b.y);
                                 } else {
-                                    mma16816(acc[nt], ka, bq[nt][kc][0], bq[nt][kc][1]);
+                                    imma_u8s8(acc[np], ka, bq[np][kw][0], bq[np][kw][1]);
                                 }
                             }
                         }
-                    }
-                    const float2 pA = __half22float2(*reinterpret_cast<const __half2*>(st + S::kOffKp + tA * S::kPairB + 4 * gam));
-                    const float2 pB = __half22float2(*reinterpret_cast<const __half2*>(st + S::kOffKp + tB * S::kPairB + 4 * gam));
+                        const float2 pA = __half22float2(*reinterpret_cast<const __half2*>(kp + 4 * gam));
+                        const float2 pB = __half22float2(*reinterpret_cast<const __half2*>(kp + 8 * S::kPairB + 4 * gam));
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const float xA = kTwoHeads ? acc[0][nt] : acc[kTwoHeads ? 0 : nt][0] + acc[kTwoHeads ? 0 : nt][1];
-                        const float xB = kTwoHeads ? acc[0][2 + nt] : acc[kTwoHeads ? 0 : nt][2] + acc[kTwoHeads ? 0 : nt][3];
-                        s0[nt] = fmaf(pA.x, xA, s0[nt]);
-                        s1[nt] = fmaf(pB.x, xB, s1[nt]);
-                        z0[nt] = fmaf(pA.y, qs[nt][gam], z0[nt]);
-                        z1[nt] = fmaf(pB.y, qs[nt][gam], z1[nt]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            // the four limbs of this lane's head (each sum below 2^22, so a pair fits 32 bits)
+                            const int(&lo_)[4] = acc[2 * nt];
+                            const int(&hi_)[4] = acc[2 * nt + 1];
+                            const float xA = fmaf((float)(hi_[0] + 256 * hi_[1]), 65536.f, (float)(lo_[0] + 256 * lo_[1]));
+                            const float xB = fmaf((float)(hi_[2] + 256 * hi_[3]), 65536.f, (float)(lo_[2] + 256 * lo_[3]));
+                            sc[nt][2 * kt] = fmaf(pA.x, xA, sc[nt][2 * kt]);
+                            sc[nt][2 * kt + 1] = fmaf(pB.x, xB, sc[nt][2 * kt + 1]);
+                            zc[nt][2 * kt] = fmaf(pA.y, qs[nt][gam], zc[nt][2 * kt]);
+                            zc[nt][2 * kt + 1] = fmaf(pB.y, qs[nt][gam], zc[nt][2 * kt + 1]);
+                        }
                     }
                 }
                 // ---- the values' scales and zeros, and a bound of log2 of the scales
-                float2 vA[NG], vB[NG];
-                float bigA = 5.9604645e-8f, bigB = 5.9604645e-8f;              // 2^-24, the least scale above zero
+                const uint8_t* vp = st + S::kOffVp + (k0 * 16 + gr) * S::kPairB;
+                uint32_t vpair[NP][NG];
+                float lg[NP];
 #pragma unroll
-                for (int gam = 0; gam < NG; ++gam) {
-                    vA[gam] = __half22float2(*reinterpret_cast<const __half2*>(st + S::kOffVp + tA * S::kPairB + 4 * gam));
-                    vB[gam] = __half22float2(*reinterpret_cast<const __half2*>(st + S::kOffVp + tB * S::kPairB + 4 * gam));
-                    bigA = fmaxf(bigA, vA[gam].x);
-                    bigB = fmaxf(bigB, vB[gam].x);
+                for (int k = 0; k < NP; ++k) {
+                    float big = 5.9604645e-8f;                // 2^-24, the least scale above zero
+#pragma unroll
+                    for (int gam = 0; gam < NG; ++gam) {
+                        vpair[k][gam] = *reinterpret_cast<const uint32_t*>(vp + 8 * k * S::kPairB + 4 * gam);
+                        big = fmaxf(big, __low2float(*reinterpret_cast<const __half2*>(&vpair[k][gam])));
+                    }
+                    lg[k] = fast_log2(big);
                 }
-                const float lgA = fast_log2(bigA), lgB = fast_log2(bigB);
                 // ---- online softmax
-                float pA[NT], pB[NT];
-                [[maybe_unused]] bool okA[NT], okB[NT];
+                float p[NT][NP];
+                [[maybe_unused]] bool ok[NT][NP];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float sA = fmaf(s0[nt], fq[nt], z0[nt]), sB = fmaf(s1[nt], fq[nt], z1[nt]);
-                    float eA = sA + lgA, eB = sB + lgB;
-                    if constexpr (PARTIAL) {
-                        okA[nt] = tok0 + tA < lim[nt];
-                        okB[nt] = tok0 + tB < lim[nt];
-                        if (!okA[nt]) { sA = -INFINITY; eA = -INFINITY; }
-                        if (!okB[nt]) { sB = -INFINITY; eB = -INFINITY; }
+                    float e = -INFINITY;
+#pragma unroll
+                    for (int k = 0; k < NP; ++k) {
+                        sc[nt][k] = fmaf(sc[nt][k], fq[nt], zc[nt][k]);
+                        if constexpr (PARTIAL) {
+                            ok[nt][k] = tok0 + (k0 * 16 + 8 * k + gr) < lim[nt];
+                            if (!ok[nt][k]) sc[nt][k] = -INFINITY;
+                            e = ok[nt][k] ? fmaxf(e, sc[nt][k] + lg[k]) : e;
+                        } else {
+                            e = fmaxf(e, sc[nt][k] + lg[k]);
+                        }
                     }
-                    float e = fmaxf(eA, eB);
                     e = fmaxf(e, __shfl_xor_sync(kFull, e, 4));
                     e = fmaxf(e, __shfl_xor_sync(kFull, e, 8));
                     e = fmaxf(e, __shfl_xor_sync(kFull, e, 16));
@@ -545,83 +595,91 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
                         const float mn = e - kRoom > mref[nt] ? e - kRoom : mref[nt];
                         const float f = mref[nt] == -INFINITY ? 0.f : fast_exp2(mref[nt] - mn);   // nothing summed so far
                         mref[nt] = mn;
+                        mexp[nt] = mn == -INFINITY ? 0.f : mn;
                         lsum[nt] *= f;
 #pragma unroll
                         for (int G_ = 0; G_ < NG; ++G_) oz[nt][G_] *= f;
 #pragma unroll
-                        for (int mt = 0; mt < kKC; ++mt) {
-                            o[nt][mt][0] *= f; o[nt][mt][1] *= f; o[nt][mt][2] *= f; o[nt][mt][3] *= f;
+                        for (int mt = 0; mt < kMT; ++mt) {
+                            if constexpr (kOneLimb) {
+                                o[0][mt][nt] *= f; o[0][mt][2 + nt] *= f;
+                            } else {
+                                o[nt][mt][0] *= f; o[nt][mt][1] *= f; o[nt][mt][2] *= f; o[nt][mt][3] *= f;
+                            }
                         }
                     }
-                    const float m = mref[nt] == -INFINITY ? 0.f : mref[nt];      // no visible token yet: s is -inf
-                    pA[nt] = fast_exp2(sA - m);
-                    pB[nt] = fast_exp2(sB - m);
-                    lsum[nt] += pA[nt] + pB[nt];
-                }
-                // ---- values: O^T += Cv^T (p vs); lane quarter t takes tokens 2t, 2t + 1 (+ 8), the
-                // odd one first where t >= 2 (bank conflicts).  An odd token enters as
-                // p (vz + 15 vs) - p vs (15 - c): codes are all positive and a long flat softmax
-                // would sum them to many times the result, with the tensor core's truncated
-                // additions (relative error against 64 bits at 4133 tokens 7e-5; this way 7e-7)
-                const float c15 = (gr & 1) ? 15.f : 0.f;      // this lane's tokens are odd
-                float qA[NT], qB[NT];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    qA[nt] = (gr & 1) ? -pA[nt] : pA[nt];
-                    qB[nt] = (gr & 1) ? -pB[nt] : pB[nt];
-                }
-#pragma unroll
-                for (int gam = 0; gam < NG; ++gam) {
-                    uint32_t pb[NT][2];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        float wA = qA[nt] * vA[gam].x, wB = qB[nt] * vB[gam].x;
-                        float yA = fmaf(vA[gam].x, c15, vA[gam].y), yB = fmaf(vB[gam].x, c15, vB[gam].y);
-                        if constexpr (PARTIAL) {              // p = 0 there, but the pair may be anything
-                            if (!okA[nt]) wA = yA = 0.f;
-                            if (!okB[nt]) wB = yB = 0.f;
-                        }
-                        oz[nt][gam] = fmaf(pA[nt], yA, fmaf(pB[nt], yB, oz[nt][gam]));
-                        uint32_t h, l;
-                        split_hilo(wA, wB, h, l);
-                        // (hi, lo) of token A and of token B: the two columns of head t
-                        pb[nt][0] = movmatrix_t(__byte_perm(h, l, 0x5410));
-                        pb[nt][1] = movmatrix_t(__byte_perm(h, l, 0x7632));
+                    for (int k = 0; k < NP; ++k) {
+                        p[nt][k] = fast_exp2(sc[nt][k] - mexp[nt]);
+                        lsum[nt] += p[nt][k];
                     }
-                    uint32_t w0[W::kV], w1[W::kV], w2[W::kV], w3[W::kV];
-                    const uint8_t* vp = st + kt * kTileB + S::kOffVc;
-                    W::value(vp + at_v0(gam), w0);
-                    W::value(vp + at_v1(gam), w1);
-                    W::value(vp + at_v0(gam) + 8 * (D / 2), w2);
-                    W::value(vp + at_v1(gam) + 8 * (D / 2), w3);
+                }
+                // ---- values: O^T += Cv^T (p vs).  An odd token enters as p (vz + 15 vs) - p vs (15 - c):
+                // codes are all positive and a long flat softmax would sum them to many times the
+                // result, with the tensor core's truncated additions (relative error against 64 bits
+                // at 4133 tokens 7e-5, this way below 5e-6)
 #pragma unroll
-                    for (int k = 0; k < W::kV; ++k) {
+                for (int kt = 0; kt < NTILE; ++kt) {
+                    uint32_t pb[VT][2];
 #pragma unroll
-                        for (int half = 0; half < (GRP == 32 ? 1 : 2); ++half) {
-                            // four values: the low halfword is token 2t's, the high one token 2t + 1's
-                            const uint32_t sel = half ? sel_hi : sel_lo;
-                            // (its 15 - c)
-                            const uint32_t x = __byte_perm(w0[k], w1[k], sel) ^ 0xffff0000u;
-                            const uint32_t y = __byte_perm(w2[k], w3[k], sel) ^ 0xffff0000u;
-                            const uint32_t x8 = x >> 8, y8 = y >> 8;
+                    for (int c2 = 0; c2 < D / 64; ++c2) {      // 64 values: two 16-byte pieces of 16 tokens
+                        uint32_t v4[4];
+                        ldsm_x4_t(smem_u32(st + (k0 + kt) * kTileB + S::kOffVc + at_v(c2)), v4);
 #pragma unroll
-                            for (int r = 0; r < 4; r += 2) {
-                                const uint32_t va[4] = {pick(x, x8, r), pick(x, x8, r + 1), pick(y, y8, r), pick(y, y8, r + 1)};
-                                const int mt = gam * (GRP / 16) + k * 4 + half * 2 + (r >> 1);
+                        for (int h = 0; h < 2; ++h) {
+                            const int c = 2 * c2 + h, gam = 32 * c / GRP;
+                            if (32 * c % GRP == 0) {           // a new group: its weights
+                                float w2[NT][2];
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][mt], va, pb[nt][0], pb[nt][1]);
+                                for (int k = 0; k < 2; ++k) {
+                                    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&vpair[2 * kt + k][gam]));
+                                    const float vs = v.x * odd;
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt) {
+                                        float w_ = p[nt][2 * kt + k] * vs, y_ = fmaf(v.x, c15, v.y);
+                                        if constexpr (PARTIAL)     // p = 0 there, but the pair may be anything
+                                            if (!ok[nt][2 * kt + k]) w_ = y_ = 0.f;
+                                        w2[nt][k] = w_;
+                                        oz[nt][gam] = fmaf(p[nt][2 * kt + k], y_, oz[nt][gam]);
+                                    }
+                                }
+                                // columns of token A and of token B: (head t, head 4 + t), or (hi, lo) of head t
+                                if constexpr (kOneLimb) {
+#pragma unroll
+                                    for (int k = 0; k < 2; ++k)
+                                        pb[0][k] = movmatrix_t(h2_bits(__floats2half2_rn(w2[0][k], NT == 2 ? w2[NT - 1][k] : 0.f)));
+                                } else {
+#pragma unroll
+                                    for (int nt = 0; nt < VT; ++nt) {
+                                        uint32_t hi, lo;
+                                        split_hilo(w2[nt][0], w2[nt][1], hi, lo);
+                                        pb[nt][0] = movmatrix_t(__byte_perm(hi, lo, 0x5410));
+                                        pb[nt][1] = movmatrix_t(__byte_perm(hi, lo, 0x7632));
+                                    }
+                                }
+                            }
+                            // registers: tokens 2t, 2t + 1 (low, high half) and 8 further on, values 32 c + 4 g ..
+                            const uint32_t x = v4[2 * h], y = v4[2 * h + 1], x8 = x >> 8, y8 = y >> 8;
+                            const uint32_t va[4] = {pick<0>(x, x8), pick<1>(x, x8), pick<0>(y, y8), pick<1>(y, y8)};
+                            const uint32_t vb[4] = {pick<2>(x, x8), pick<3>(x, x8), pick<2>(y, y8), pick<3>(y, y8)};
+#pragma unroll
+                            for (int vt = 0; vt < VT; ++vt) {
+                                mma16816(o[vt][2 * c], va, pb[vt][0], pb[vt][1]);
+                                mma16816(o[vt][2 * c + 1], vb, pb[vt][0], pb[vt][1]);
                             }
                         }
                     }
                 }
             };
             if (tok0 + CH <= minlim) {
+                constexpr int kTogether = S::kTogether;
 #pragma unroll
-                for (int kt = 0; kt < S::kTiles; ++kt) tile(kt, std::false_type{});
+                for (int k0 = 0; k0 < S::kTiles; k0 += kTogether)
+                    tiles(std::integral_constant<int, kTogether>{}, k0, std::false_type{});
             } else {
 #pragma unroll 1
-                for (int kt = 0; kt < S::kTiles; ++kt)
-                    if (tok0 + 16 * kt < len) tile(kt, std::true_type{});
+                for (int k0 = 0; k0 < S::kTiles; ++k0)
+                    if (tok0 + 16 * k0 < len) tiles(std::integral_constant<int, 1>{}, k0, std::true_type{});
             }
             __syncwarp();
             if (i + RING < nmine) {
@@ -652,12 +710,13 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
             if (mref[nt] != -INFINITY) {
                 float* dst = sAcc + (warp * ROWS + h) * D;
 #pragma unroll
-                for (int mt = 0; mt < kKC; ++mt) {
-                    const int gam = mt / (GRP / 16), in = mt % (GRP / 16);
-                    // values 2 (in % 2 or 4) of this lane row's run of GRP / 8 values of the group
-                    const int val = gam * GRP + gr * (GRP / 8) + 2 * in;
-                    dst[val] = fmaf(o[nt][mt][0] + o[nt][mt][1], kTwo24, oz[nt][gam]);
-                    dst[val + 1] = fmaf(o[nt][mt][2] + o[nt][mt][3], kTwo24 / 16.f, oz[nt][gam]);
+                for (int mt = 0; mt < kMT; ++mt) {
+                    // tile mt: values 2 (mt % 2) and one more of lane row g's four in the 32 of piece mt / 2
+                    const int gam = 16 * mt / GRP, val = 32 * (mt >> 1) + 4 * gr + 2 * (mt & 1);
+                    const float x = kOneLimb ? o[0][mt][nt] : o[kOneLimb ? 0 : nt][mt][0] + o[kOneLimb ? 0 : nt][mt][1];
+                    const float y = kOneLimb ? o[0][mt][2 + nt] : o[kOneLimb ? 0 : nt][mt][2] + o[kOneLimb ? 0 : nt][mt][3];
+                    dst[val] = fmaf(x, kTwo24, oz[nt][gam]);
+                    dst[val + 1] = fmaf(y, kTwo24 / 16.f, oz[nt][gam]);
                 }
             }
         }

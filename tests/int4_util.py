@@ -11,8 +11,11 @@ factor of at most 1 + 2 eps_s relative to the sum, and by the exponential and th
 22-bit limbs (2^-21) and the fp32 sums (at most 2^-19), so an output is off by
 V (2 eps_s + 2^-18), V = the largest |value|, plus half a step of its type.
 
-bf16 calls with more than 8 query rows per kv head round K, V and P to fp16 as
-well (half a step is 2^-11): eps_s grows by 2^-11 S and the output by 2 2^-11 V
+bf16 outputs take rounded weights (`bf16`): with up to 8 query rows per kv head the
+products p vs of weight and value scale are fp16 numbers, off by half a step, 2^-11
+of themselves, so the output is off by at most 2^-11 times the largest code part
+15 vs <= max v - min v <= 2 V of its tokens: 2^-10 V.  With more rows P and V are
+rounded to fp16: 2 2^-11 V, the same; and K is too, so eps_s grows by 2^-11 S
 (`rounded`)."""
 import numpy as np
 
@@ -78,10 +81,10 @@ def attend(q, k, v, scale, n_q):
     return out
 
 
-def attend_bound(q, kabs, v, scale, out, half_step, rounded=False):
+def attend_bound(q, kabs, v, scale, out, half_step, bf16=False, rounded=False):
     """Largest allowed |error| of the outputs [Lq, d]; kabs [T, d]: |zero| + |scale c|."""
     if len(v) == 0:
         return np.zeros_like(out)
     S = abs(scale) * (np.abs(q) @ kabs.T).max(-1, keepdims=True)
     eps_s = S * (2.0 ** -19 + (2.0 ** -11 if rounded else 0.0))
-    return np.abs(v).max() * (2 * eps_s + 2.0 ** -18 + (2.0 ** -10 if rounded else 0.0)) + half_step * np.abs(out) + 1e-30
+    return np.abs(v).max() * (2 * eps_s + 2.0 ** -18 + (2.0 ** -10 if bf16 else 0.0)) + half_step * np.abs(out) + 1e-30

@@ -269,7 +269,8 @@ def run_attend(d, group, dtype, G, Hkv, lens, Lq=1, paged=False, uniform=False, 
                 rows = qn[b, :, hh * G + g]
                 ref = U.attend(rows, k, v, scale, Lq)
                 err = np.abs(got[b, :, hh * G + g] - ref)
-                bound = U.attend_bound(rows, kabs, v, scale, ref, half, rounded=dtype == "bf16" and Lq * G > 8)
+                bound = U.attend_bound(rows, kabs, v, scale, ref, half, bf16=dtype == "bf16",
+                                       rounded=dtype == "bf16" and Lq * G > 8)
                 if dtype == "f16":
                     bound = bound + 2.0 ** -25        # half a subnormal step
                 assert np.isfinite(got[b, :, hh * G + g]).all()
