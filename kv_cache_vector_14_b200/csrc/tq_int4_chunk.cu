@@ -462,6 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             }
             float mref = -INFINITY, lsum = 0.f;
             bool any = false;                                  // this stream has an O
+            const bool idle = !__any_sync(kFull, rvalid);      // none of the warp's rows is there
             const uint64_t fr2 = pack2(fr, fr);
             for (int jj = MT == 2 ? j : j + ((j & 1) ^ x); jj < j1 && !failed; jj += 3 - MT) {
                 const int b = 2 * x + (nS & 1);                // score buffer
@@ -471,6 +472,11 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 if (!warp_wait(bar(kBarS + b), (uint32_t)((nS >> 1) & 1))) { failed = true; break; }
                 ++nS;
                 tc_fence_after();
+                if (idle) {                                    // P of these rows may be anything: O's other rows do not see it
+                    tc_fence_before();
+                    mbar_arrive(bar(kBarP + b));
+                    continue;
+                }
                 uint32_t sv[TT];
                 tc_ld64(tx, sv);
                 if (vis < TT) {
