@@ -19,8 +19,7 @@
 // are the two row tiles of the unit, and an expanded tile serves 256 rows; with MT = 1
 // (few rows, or fp32 at head_dim 128, whose query limbs leave no shared memory) they
 // take the even and the odd tiles and are merged at the unit's end.  Warps 8-11
-// expand the blocks, K and V of a tile in turn, warp 13 fills their ring (bulk
-// copies), warp 12 issues the mma (one thread), the scores of the next tiles before
+// expand the blocks, warp 13 fills their ring (bulk copies), warp 12 issues the mma (one thread), the scores of the next tiles before
 // the values of this one, so that softmax and tensor core overlap.  The mma of one
 // thread run in issue order, so a score buffer is not overwritten before the product
 // with the weights in it has run.  The reference exponent moves only when it is
@@ -47,7 +46,7 @@ namespace {
 constexpr int kSoft = 256;                // softmax threads: two streams x 128 rows
 constexpr int kProd = 128;                // producer threads
 constexpr int kThreads = kSoft + kProd + 64;
-constexpr int kSlots = 6;                 // ring of raw cache blocks (64 tokens of K or of V)
+constexpr int kSlots = 3;                 // ring of raw tiles (a K and a V block)
 constexpr float kRoom = 7.f, kLazy = 8.f; // P is kept below 2^15 (fp16 holds 65504)
 
 template <int D, int GRP, int NL, int QL, int MT>
@@ -61,7 +60,7 @@ struct Ch {
     static constexpr int kBuf = 2 * NL * kTile;               // K limbs, V limbs
     static constexpr int kOffQ = kBufs * kBuf;                    // [MT][QL]
     static constexpr int kOffRing = kOffQ + MT * QL * kQ;
-    static constexpr int kOffBar = kOffRing + kSlots * kBlockB;
+    static constexpr int kOffBar = kOffRing + kSlots * 2 * kBlockB;
     static constexpr int kOffXch = kOffBar + 38 * 8;          // [2][2][128]: reference, sum
     static constexpr int kOffBad = kOffXch + 4 * 128 * 4;     // [4 segments][4 groups]: first non-finite token
     static constexpr int kOffScan = kOffBad + 16 * 4;         // [kThreads / 32 + 3] int64
@@ -78,12 +77,10 @@ struct Ch {
 // mbarriers.  A barrier is never two phases ahead of a thread that waits on it: whatever a
 // stream's two score buffers allow to run ahead has a barrier per buffer.
 enum : int {
-    kBarRing = 0,      // [6] a raw block in its slot (copy bytes)
-    kBarSlot = 6,      // [6] a raw block read (kProd arrivals)
-    kBarKReady = 12,   // [3] K operand of a buffer built (kProd arrivals)
-    kBarVReady = 15,   // [3] V operand
-    kBarKFree = 18,    // [3] K operand read (commit)
-    kBarVFree = 21,    // [3] V operand read (commit)
+    kBarRing = 0,      // [3] a tile's raw K and V blocks in their slot (copy bytes)
+    kBarSlot = 3,      // [3] a slot read (kProd arrivals)
+    kBarReady = 6,     // [3] operands of a buffer built (kProd arrivals)
+    kBarFree = 9,      // [3] operands of a buffer read (commit)
     kBarS = 24,        // [2][2] S of stream x, score buffer b computed (commit)
     kBarP = 28,        // [2][2] P of stream x in score buffer b written (128 arrivals)
     kBarO = 32,        // [2] O of stream x updated (commit)
@@ -172,12 +169,6 @@ __device__ __forceinline__ bool soft_or(bool v) {
     return r != 0;
 }
 template <int DT>
-__device__ __forceinline__ float q_elem(const void* p, int64_t i) {
-    if constexpr (DT == TQ_F32) return __ldg(static_cast<const float*>(p) + i);
-    else if constexpr (DT == TQ_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-    else return __half2float(static_cast<const __half*>(p)[i]);
-}
-template <int DT>
 __device__ __forceinline__ void put_elem(void* p, int64_t i, float x) {
     if constexpr (DT == TQ_F32) static_cast<float*>(p)[i] = x;
     else if constexpr (DT == TQ_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
@@ -230,34 +221,34 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// N consecutive elements of a row as floats; vec: the row is 16-byte aligned
+// N consecutive elements of a row as stored (zeros where there is no row); vec: the row is 16-byte aligned
 template <int DT, int N>
-__device__ __forceinline__ void load_row(const void* p, int64_t at, bool vec, float (&v)[N]) {
-    constexpr int kE = DT == TQ_F32 ? 4 : 2;
+__device__ __forceinline__ void load_raw(const void* p, int64_t at, bool vec, bool there, uint32_t (&w)[N * (DT == TQ_F32 ? 4 : 2) / 4]) {
+    constexpr int kE = DT == TQ_F32 ? 4 : 2, kN = N * kE / 4;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) w[i] = 0u;
+    if (!there) return;
+    const char* s = static_cast<const char*>(p) + at * kE;
     if (vec) {
-        const uint4* s = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * kE);
 #pragma unroll
-        for (int i = 0; i < N * kE / 16; ++i) {
-            const uint4 u = __ldg(s + i);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if constexpr (DT == TQ_F32) {
-                    v[4 * i + k] = __uint_as_float(w[k]);
-                } else if constexpr (DT == TQ_BF16) {
-                    v[8 * i + 2 * k] = __uint_as_float(w[k] << 16);
-                    v[8 * i + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-                } else {
-                    const float2 f = __half22float2(as_h2(w[k]));
-                    v[8 * i + 2 * k] = f.x;
-                    v[8 * i + 2 * k + 1] = f.y;
-                }
-            }
+        for (int i = 0; i < kN / 4; ++i) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(s) + i);
+            w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
         }
-    } else {
+    } else if constexpr (DT == TQ_F32) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = q_elem<DT>(p, at + i);
+        for (int i = 0; i < kN; ++i) w[i] = reinterpret_cast<const uint32_t*>(s)[i];
+    } else {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(s);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) w[i] = (uint32_t)h[2 * i] | ((uint32_t)h[2 * i + 1] << 16);
     }
+}
+template <int DT, int N>
+__device__ __forceinline__ float raw_elem(const uint32_t (&w)[N], int e) {
+    if constexpr (DT == TQ_F32) return __uint_as_float(w[e]);
+    else if constexpr (DT == TQ_BF16) return __uint_as_float((e & 1) ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+    else return (e & 1) ? __high2float(as_h2(w[e >> 1])) : __low2float(as_h2(w[e >> 1]));
 }
 // eight consecutive outputs
 template <int DT>
@@ -309,10 +300,8 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             mbar_init(bar(kBarSlot + i), kProd);
         }
         for (int i = 0; i < C::kBufs; ++i) {
-            mbar_init(bar(kBarKReady + i), kProd);
-            mbar_init(bar(kBarVReady + i), kProd);
-            mbar_init(bar(kBarKFree + i), 1);
-            mbar_init(bar(kBarVFree + i), 1);
+            mbar_init(bar(kBarReady + i), kProd);
+            mbar_init(bar(kBarFree + i), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(kBarO + i), 1);
@@ -415,16 +404,12 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             // position p of a word's eight holds value word_value(p), as in the expanded operands
             float fr;
             {
+                constexpr int kRegs = kCols * (DT == TQ_F32 ? 4 : 2) / 4;        // the row part as stored
+                uint32_t raw_q[kRegs];
+                load_raw<DT, kCols>(a.q, qrow * D + col0, a.vec16, rvalid, raw_q);
                 float mx = 0.f;
-                if (rvalid) {
 #pragma unroll
-                    for (int e0 = 0; e0 < kCols; e0 += 16) {
-                        float v[16];
-                        load_row<DT, 16>(a.q, qrow * D + col0 + e0, a.vec16, v);
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) mx = fmaxf(mx, fabsf(v[e]));
-                    }
-                }
+                for (int e = 0; e < kCols; ++e) mx = fmaxf(mx, fabsf(raw_elem<DT>(raw_q, e)));
                 if constexpr (MT == 1) {
                     xch[x * 128 + r] = mx;
                     soft_or(false);
@@ -436,26 +421,16 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 const float fs = a.scale_log2 < 0.f ? -f : f;
                 fr = fmaxf(fabsf(a.scale_log2) / f, 1e-37f);  // (above zero: a masked -inf stays one)
                 uint8_t* sq = sm + C::kOffQ + (MT == 2 ? x * QL * C::kQ : 0);
-#pragma unroll 1
-                for (int c0 = 0; c0 < kCols; c0 += 16) {
-                    float v[16];
-                    if (rvalid) {
-                        load_row<DT, 16>(a.q, qrow * D + col0 + c0, a.vec16, v);
-                    } else {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = 0.f;
-                    }
+                for (int i = 0; i < kCols; i += 8) {           // eight positions, 16 bytes
+                    uint32_t qh[4], qlo[4];
 #pragma unroll
-                    for (int i = 0; i < 16; i += 8) {          // eight positions, 16 bytes
-                        uint32_t qh[4], qlo[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            split_hilo(v[i + word_value(2 * k)] * fs, v[i + word_value(2 * k + 1)] * fs, qh[k], qlo[k]);
-                        const uint32_t at = sw128_byte(r, 2 * (col0 + c0 + i), 128);
-                        *reinterpret_cast<uint4*>(sq + at) = make_uint4(qh[0], qh[1], qh[2], qh[3]);
-                        if constexpr (QL == 2)
-                            *reinterpret_cast<uint4*>(sq + C::kQ + at) = make_uint4(qlo[0], qlo[1], qlo[2], qlo[3]);
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        split_hilo(raw_elem<DT>(raw_q, i + word_value(2 * k)) * fs, raw_elem<DT>(raw_q, i + word_value(2 * k + 1)) * fs,
+                                   qh[k], qlo[k]);
+                    const uint32_t at = sw128_byte(r, 2 * (col0 + i), 128);
+                    *reinterpret_cast<uint4*>(sq + at) = make_uint4(qh[0], qh[1], qh[2], qh[3]);
+                    if constexpr (QL == 2) *reinterpret_cast<uint4*>(sq + C::kQ + at) = make_uint4(qlo[0], qlo[1], qlo[2], qlo[3]);
                 }
                 fence_proxy_async();
                 mbar_arrive(bar(kBarQ));
@@ -634,45 +609,45 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
         uint32_t at[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) at[i] = sw128_byte(tau0, 2 * (32 * cp + 8 * i), TT);
+        // (no warp-collective instruction here: a thread whose wait runs out leaves, the others follow)
         int slot = 0, sp = 0, bf = 0, bfp = 0, seg = 0;        // ring slot and buffer, with their phases
-        for (int i = 0; i < 2 * J; ++i) {
-            const int side = i & 1;                            // 0: K, 1: V
-            if (!warp_wait(bar(kBarRing + slot), (uint32_t)sp)) { failed = true; break; }
-            const uint8_t* raw_blk = sm + C::kOffRing + slot * C::kBlockB;
+        for (int j = 0; j < J; ++j) {
+            if (!mbar_wait_bounded(bar(kBarRing + slot), (uint32_t)sp)) { failed = true; break; }
+            const uint8_t* raw_blk = sm + C::kOffRing + slot * 2 * C::kBlockB;
             const int64_t tok0 = (int64_t)w.k * TT, inside = w.n - tok0;
             const int valid = inside < TT ? (int)(inside > 0 ? inside : 0) : TT;           // tokens inside the sequence
-            uint4 v[kItems];
-            uint32_t bits[kItems];
+            // items: K, then V
+            uint4 v[2 * kItems];
+            uint32_t bits[2 * kItems];
             bool rare = false;
 #pragma unroll
-            for (int it = 0; it < kItems; ++it) {
-                v[it] = *reinterpret_cast<const uint4*>(raw_blk + src + 32 * it * (D / 2));
-                bits[it] = *reinterpret_cast<const uint32_t*>(raw_blk + prs + 32 * it * NG * 4);
-                if (tau0 + 32 * it >= valid) bits[it] = 0u;    // behind the sequence anything may stand
+            for (int it = 0; it < 2 * kItems; ++it) {
+                const uint8_t* blk = raw_blk + (it / kItems) * C::kBlockB;
+                const int dt = 32 * (it % kItems);
+                v[it] = *reinterpret_cast<const uint4*>(blk + src + dt * (D / 2));
+                bits[it] = *reinterpret_cast<const uint32_t*>(blk + prs + dt * NG * 4);
+                if (tau0 + dt >= valid) bits[it] = 0u;         // behind the sequence anything may stand
                 // a scale of 2^11 or more, a zero of 2^15 or more, infinity or NaN
                 rare |= (bits[it] & 0x7fffu) >= 0x6800u || (bits[it] & 0x7fff0000u) >= 0x78000000u;
             }
-            if (i >= 2 * C::kBufs && !warp_wait(bar((side ? kBarVFree : kBarKFree) + bf), (uint32_t)(bfp ^ 1))) {
-                failed = true;
-                break;
-            }
+            if (j >= C::kBufs && !mbar_wait_bounded(bar(kBarFree + bf), (uint32_t)(bfp ^ 1))) { failed = true; break; }
             if (rare) {                                        // (after the wait: it bounds how far ahead marks are made)
 #pragma unroll
-                for (int it = 0; it < kItems; ++it) {
-                    if (side && ((bits[it] & 0x7c00u) == 0x7c00u || (bits[it] & 0x7c000000u) == 0x7c000000u)) {
+                for (int it = 0; it < 2 * kItems; ++it) {
+                    if (it >= kItems && ((bits[it] & 0x7c00u) == 0x7c00u || (bits[it] & 0x7c000000u) == 0x7c000000u)) {
                         bits[it] = 0u;
-                        atomicMin(&sBad[4 * (seg & 3) + gam], (int)tok0 + tau0 + 32 * it);
+                        atomicMin(&sBad[4 * (seg & 3) + gam], (int)tok0 + tau0 + 32 * (it % kItems));
                     }
                     // the largest value stays finite in fp16
                     if (fmaf(15.f, __low2float(as_h2(bits[it])), __high2float(as_h2(bits[it]))) > 65504.f) bits[it] -= 1u;
                 }
             }
-            uint8_t* buf = sm + bf * C::kBuf + side * NL * C::kTile;
+            uint8_t* buf = sm + bf * C::kBuf;
 #pragma unroll
-            for (int it = 0; it < kItems; ++it) {
+            for (int it = 0; it < 2 * kItems; ++it) {
                 const __half2 s2 = __low2half2(as_h2(bits[it])), z2 = __high2half2(as_h2(bits[it]));
                 const uint32_t wd[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
-                uint8_t* op = buf + 32 * it * 128;             // (32 rows further: 4 atoms of 1024 bytes)
+                uint8_t* op = buf + (it / kItems) * NL * C::kTile + 32 * (it % kItems) * 128;    // (32 rows: 4 atoms of 1024 bytes)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t h[4], l[4];
@@ -681,22 +656,21 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                     if constexpr (NL == 2) *reinterpret_cast<uint4*>(op + C::kTile + at[i]) = make_uint4(l[0], l[1], l[2], l[3]);
                 }
             }
-            fence_proxy_async();           // operands for the tensor core; the slot's reads before its next copy
+            fence_proxy_async();           // operands for the tensor core; the slot's reads before its next copies
+            mbar_arrive(bar(kBarReady + bf));
             mbar_arrive(bar(kBarSlot + slot));
-            mbar_arrive(bar((side ? kBarVReady : kBarKReady) + bf));
             if (++slot == kSlots) { slot = 0; sp ^= 1; }
-            if (!side) continue;
             if (++bf == C::kBufs) { bf = 0; bfp ^= 1; }
             if (w.k == w.nt - 1) ++seg;
             w.next(a);
         }
-        if (failed && lane == 0) atomicExch(a.err, 1);
+        if (failed) atomicExch(a.err, 1);
     } else if (warp == 13) {
         // ======================================== loader: one thread fills the ring, K and V block
         // of each tile
         if (lane == 0) {
             W w = w0;
-            int i = 0, slot = 0, sp = 0;                       // blocks loaded
+            int i = 0, slot = 0, sp = 0;                       // tiles loaded
             asm volatile("fence.proxy.async;" ::: "memory");
             for (int j = 0; j < J && !failed; ++j) {
                 const int64_t bh = (int64_t)w.b * a.Hkv + w.kv;
@@ -705,16 +679,15 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                     blk[0] = cache_block(a.ktable, a.kpool, a.NB, bh, w.k, a.err);
                     blk[1] = cache_block(a.vtable, a.vpool, a.NB, bh, w.k, a.err);
                 }
+                if (i >= kSlots && !mbar_wait_bounded(bar(kBarSlot + slot), (uint32_t)(sp ^ 1))) { failed = true; break; }
+                const uint32_t br = bar(kBarRing + slot);
+                mbar_expect_tx(br, (uint32_t)(2 * C::kBlockB));
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    if (i >= kSlots && !mbar_wait_bounded(bar(kBarSlot + slot), (uint32_t)(sp ^ 1))) { failed = true; break; }
-                    const uint32_t br = bar(kBarRing + slot);
-                    mbar_expect_tx(br, (uint32_t)C::kBlockB);
-                    bulk_g2s(smem_u32(sm + C::kOffRing + slot * C::kBlockB),               // a bad table entry reads block 0
+                for (int k = 0; k < 2; ++k)                    // a bad table entry reads block 0
+                    bulk_g2s(smem_u32(sm + C::kOffRing + (2 * slot + k) * C::kBlockB),
                              (k ? a.vc : a.kc) + (blk[k] >= 0 ? blk[k] : 0) * C::kBlockB, C::kBlockB, br);
-                    ++i;
-                    if (++slot == kSlots) { slot = 0; sp ^= 1; }
-                }
+                ++i;
+                if (++slot == kSlots) { slot = 0; sp ^= 1; }
                 w.next(a);
             }
             // copies that may still be in flight (the last one into each slot)
@@ -733,7 +706,7 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
         const uint64_t vdesc = sw128_desc_mn(sbase + NL * C::kTile, (uint32_t)(TT * 128), 1024u);
         int nS[2] = {0, 0}, nP[2] = {0, 0};    // S issued and P taken of each stream so far
         // S of stream x from buffer bf
-        auto mma_s = [&](int x, int bf, bool last) {
+        auto mma_s = [&](int x, int bf) {
             const uint64_t kd = kdesc + (uint64_t)(bf * (C::kBuf >> 4));
             const uint64_t qd = qdesc + (uint64_t)(MT == 2 ? x * ((QL * C::kQ) >> 4) : 0);
             const int b = 2 * x + (nS[x]++ & 1);                // score buffer
@@ -751,7 +724,6 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 }
             }
             commit(bar(kBarS + b));
-            if (last) commit(bar(kBarKFree + bf));          // the tile's last use of K
         };
         // O of stream x (+)= P V from buffer bf, once P is there
         auto mma_o = [&](int x, int bf, bool first, bool last) -> bool {
@@ -772,39 +744,39 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 }
             }
             commit(bar(kBarO + x));
-            if (last) commit(bar(kBarVFree + bf));          // the tile's last use of V
+            if (last) commit(bar(kBarFree + bf));           // the tile's last product
             return true;
         };
-        // S of tile j (both row tiles, or the tile's stream), once K is there
-        constexpr int kAhead = MT == 2 ? 1 : 2;                // tiles whose scores go out before this one's values
-        int sb = 0, sbp = 0;               // next K buffer and its phase
+        // S of tile j (both row tiles, or the tile's stream), once its operands are there
+        // tiles whose scores go out before this one's values (fewer than there are buffers)
+        constexpr int kAhead = MT == 2 || C::kBufs == 2 ? 1 : 2;
+        int sb = 0, sbp = 0;               // buffer of the next scores, and its phase
         auto scores = [&](int j) -> bool {
-            if (!warp_wait(bar(kBarKReady + sb), (uint32_t)sbp)) return false;
+            if (!warp_wait(bar(kBarReady + sb), (uint32_t)sbp)) return false;
             tc_fence_after();
             if constexpr (MT == 2) {
-                mma_s(0, sb, false);
-                mma_s(1, sb, true);
+                mma_s(0, sb);
+                mma_s(1, sb);
             } else {
-                mma_s(j & 1, sb, true);
+                mma_s(j & 1, sb);
             }
             if (++sb == C::kBufs) { sb = 0; sbp ^= 1; }
             return true;
         };
-        int vb = 0, vbp = 0;               // next V buffer and its phase
+        int vb = 0;                        // buffer of the next values (its scores have waited for it)
         for (int j = 0, seg = 0; j < J && ok; ++seg) {
             const int left = w.nt - w.k, j1 = j + left < J ? j + left : J;     // the segment's tiles
             if (!(ok = warp_wait(bar(kBarQ), (uint32_t)(seg & 1)))) break;
             for (int i = 0; i < kAhead && j + i < j1 && ok; ++i) ok = scores(j + i);
             for (int i = j; i < j1 && ok; ++i) {
                 if (i + kAhead < j1 && !(ok = scores(i + kAhead))) break;
-                if (!(ok = warp_wait(bar(kBarVReady + vb), (uint32_t)vbp))) break;
                 if constexpr (MT == 2) {
                     if (!(ok = mma_o(0, vb, i == j, false))) break;
                     if (!(ok = mma_o(1, vb, i == j, true))) break;
                 } else {
                     if (!(ok = mma_o(i & 1, vb, i - j < 2, true))) break;
                 }
-                if (++vb == C::kBufs) { vb = 0; vbp ^= 1; }
+                if (++vb == C::kBufs) vb = 0;
             }
             if (ok) {
                 commit(bar(kBarSeg));
