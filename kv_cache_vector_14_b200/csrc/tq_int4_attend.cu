@@ -55,8 +55,8 @@ struct Shape {
     static constexpr int kCodeB = D / 2, kPairB = 4 * kNG;    // bytes per token
     static constexpr int kChunk = D <= 128 ? 32 : 16;         // tokens per ring stage
     static constexpr int kTiles = kChunk / 16;
-    static constexpr int kNW = (NT == 1 && D <= 128) ? 16 : 8;
-    static constexpr int kRing = (NT == 1 && D <= 128) ? 2 : (D <= 128 ? 4 : 3);
+    static constexpr int kNW = (NT == 1 && D <= 128) ? 12 : 8;
+    static constexpr int kRing = (NT == 1 || D == 256) ? 3 : 4;
     static constexpr int kOffKc = 0;
     static constexpr int kOffKp = kChunk * kCodeB;
     static constexpr int kOffVc = kOffKp + kChunk * kPairB;
@@ -771,7 +771,7 @@ cudaError_t launch_t(const Int4AttendArgs& a, int num_sms, cudaStream_t s) {
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) return e;
-    return launch_int4_combine<D, DT>(a, S::kRows, false, ctas, s);
+    return launch_int4_combine<D, DT>(a, S::kRows, ctas, s);
 }
 template <int D, int GRP>
 cudaError_t launch_g(tq_dtype dt, const Int4AttendArgs& a, int num_sms, cudaStream_t s) {

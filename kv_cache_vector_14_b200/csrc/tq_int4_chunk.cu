@@ -53,7 +53,7 @@ template <int D, int GRP, int NL, int QL, int MT>
 struct Ch {
     static constexpr int kNG = D / GRP;
     static constexpr int TT = 64;                             // tokens per tile: one cache block
-    static constexpr int kBufs = NL == 1 ? 3 : 2;             // operand buffers
+    static constexpr int kBufs = NL == 2 ? 2 : MT == 2 ? 3 : 5;   // operand buffers: what shared memory holds
     static constexpr int kBlockB = 64 * (D / 2 + 4 * kNG);
     static constexpr int kTile = TT * D * 2;                  // one fp16 operand of a tile
     static constexpr int kQ = 128 * D * 2;                    // one limb of a row tile's queries
@@ -62,8 +62,8 @@ struct Ch {
     static constexpr int kOffRing = kOffQ + MT * QL * kQ;
     static constexpr int kOffBar = kOffRing + kSlots * 2 * kBlockB;
     static constexpr int kOffXch = kOffBar + 38 * 8;          // [2][2][128]: reference, sum
-    static constexpr int kOffBad = kOffXch + 4 * 128 * 4;     // [4 segments][4 groups]: first non-finite token
-    static constexpr int kOffScan = kOffBad + 16 * 4;         // [kThreads / 32 + 3] int64
+    static constexpr int kOffBad = kOffXch + 4 * 128 * 4;     // [8 segments][4 groups]: first non-finite token
+    static constexpr int kOffScan = kOffBad + 32 * 4;         // [kThreads / 32 + 3] int64
     static constexpr int kOffMisc = kOffScan + (kThreads / 32 + 3) * 8;
     static constexpr int kSmem = kOffMisc + 16 + 1024;        // + slack to align the base
     static_assert(kOffRing % 16 == 0 && kOffBar % 8 == 0 && kOffScan % 8 == 0, "alignment");
@@ -79,14 +79,14 @@ struct Ch {
 enum : int {
     kBarRing = 0,      // [3] a tile's raw K and V blocks in their slot (copy bytes)
     kBarSlot = 3,      // [3] a slot read (kProd arrivals)
-    kBarReady = 6,     // [3] operands of a buffer built (kProd arrivals)
-    kBarFree = 9,      // [3] operands of a buffer read (commit)
-    kBarS = 24,        // [2][2] S of stream x, score buffer b computed (commit)
-    kBarP = 28,        // [2][2] P of stream x in score buffer b written (128 arrivals)
-    kBarO = 32,        // [2] O of stream x updated (commit)
-    kBarSeg = 34,      // O of a segment complete (commit), and the mma thread's own arrival
-    kBarQ = 35,        // query operand written (256 arrivals)
-    kBarDrain = 36,    // every mma done (commit, at exit)
+    kBarReady = 6,     // [5] operands of a buffer built (kProd arrivals)
+    kBarFree = 11,     // [5] operands of a buffer read (commit)
+    kBarS = 16,        // [2][2] S of stream x, score buffer b computed (commit)
+    kBarP = 20,        // [2][2] P of stream x in score buffer b written (128 arrivals)
+    kBarO = 24,        // [2] O of stream x updated (commit)
+    kBarSeg = 26,      // O of a segment complete (commit), and the mma warp's own arrival
+    kBarQ = 27,        // query operand written (256 arrivals)
+    kBarDrain = 28,    // every mma done (commit, at exit)
 };
 
 // tokens that the last row of row tile rt sees, and the tiles they take (at least one)
@@ -221,34 +221,36 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// N consecutive elements of a row as stored (zeros where there is no row); vec: the row is 16-byte aligned
-template <int DT, int N>
-__device__ __forceinline__ void load_raw(const void* p, int64_t at, bool vec, bool there, uint32_t (&w)[N * (DT == TQ_F32 ? 4 : 2) / 4]) {
-    constexpr int kE = DT == TQ_F32 ? 4 : 2, kN = N * kE / 4;
+// eight consecutive elements of a row (zeros where there is no row); vec: 16-byte aligned
+template <int DT>
+__device__ __forceinline__ void load8(const void* p, int64_t at, bool vec, bool there, float (&v)[8]) {
+    constexpr int kE = DT == TQ_F32 ? 4 : 2;
+    uint32_t w[2 * kE];
 #pragma unroll
-    for (int i = 0; i < kN; ++i) w[i] = 0u;
-    if (!there) return;
+    for (int i = 0; i < 2 * kE; ++i) w[i] = 0u;
     const char* s = static_cast<const char*>(p) + at * kE;
-    if (vec) {
+    if (there && vec) {
 #pragma unroll
-        for (int i = 0; i < kN / 4; ++i) {
+        for (int i = 0; i < kE / 2; ++i) {
             const uint4 u = __ldg(reinterpret_cast<const uint4*>(s) + i);
             w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
         }
-    } else if constexpr (DT == TQ_F32) {
+    } else if (there) {
+        if constexpr (DT == TQ_F32) {
 #pragma unroll
-        for (int i = 0; i < kN; ++i) w[i] = reinterpret_cast<const uint32_t*>(s)[i];
-    } else {
-        const uint16_t* h = reinterpret_cast<const uint16_t*>(s);
+            for (int i = 0; i < 8; ++i) w[i] = reinterpret_cast<const uint32_t*>(s)[i];
+        } else {
+            const uint16_t* h = reinterpret_cast<const uint16_t*>(s);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) w[i] = (uint32_t)h[2 * i] | ((uint32_t)h[2 * i + 1] << 16);
+            for (int i = 0; i < 4; ++i) w[i] = (uint32_t)h[2 * i] | ((uint32_t)h[2 * i + 1] << 16);
+        }
     }
-}
-template <int DT, int N>
-__device__ __forceinline__ float raw_elem(const uint32_t (&w)[N], int e) {
-    if constexpr (DT == TQ_F32) return __uint_as_float(w[e]);
-    else if constexpr (DT == TQ_BF16) return __uint_as_float((e & 1) ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
-    else return (e & 1) ? __high2float(as_h2(w[e >> 1])) : __low2float(as_h2(w[e >> 1]));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (DT == TQ_F32) v[i] = __uint_as_float(w[i]);
+        else if constexpr (DT == TQ_BF16) v[i] = __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+        else v[i] = (i & 1) ? __high2float(as_h2(w[i >> 1])) : __low2float(as_h2(w[i >> 1]));
+    }
 }
 // eight consecutive outputs
 template <int DT>
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
         fence_mbar_init();
     }
     int* sBad = reinterpret_cast<int*>(sm + C::kOffBad);
-    if (tid < 16) sBad[tid] = INT_MAX;
+    if (tid < 32) sBad[tid] = INT_MAX;
     if (warp == 0) {
         tc_alloc(smem_u32(tmem_slot), 512);
         tc_relinquish();
@@ -404,12 +406,16 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             // position p of a word's eight holds value word_value(p), as in the expanded operands
             float fr;
             {
-                constexpr int kRegs = kCols * (DT == TQ_F32 ? 4 : 2) / 4;        // the row part as stored
-                uint32_t raw_q[kRegs];
-                load_raw<DT, kCols>(a.q, qrow * D + col0, a.vec16, rvalid, raw_q);
+                // (two passes over the row, the second from the cache, in short loops: a unit's start and end
+                // run once per unit and are bound by fetching their instructions)
                 float mx = 0.f;
+#pragma unroll 4
+                for (int i = 0; i < kCols; i += 8) {
+                    float v[8];
+                    load8<DT>(a.q, qrow * D + col0 + i, a.vec16, rvalid, v);
 #pragma unroll
-                for (int e = 0; e < kCols; ++e) mx = fmaxf(mx, fabsf(raw_elem<DT>(raw_q, e)));
+                    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[e]));
+                }
                 if constexpr (MT == 1) {
                     xch[x * 128 + r] = mx;
                     soft_or(false);
@@ -421,13 +427,13 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 const float fs = a.scale_log2 < 0.f ? -f : f;
                 fr = fmaxf(fabsf(a.scale_log2) / f, 1e-37f);  // (above zero: a masked -inf stays one)
                 uint8_t* sq = sm + C::kOffQ + (MT == 2 ? x * QL * C::kQ : 0);
-#pragma unroll
+#pragma unroll 2
                 for (int i = 0; i < kCols; i += 8) {           // eight positions, 16 bytes
+                    float v[8];
+                    load8<DT>(a.q, qrow * D + col0 + i, a.vec16, rvalid, v);
                     uint32_t qh[4], qlo[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        split_hilo(raw_elem<DT>(raw_q, i + word_value(2 * k)) * fs, raw_elem<DT>(raw_q, i + word_value(2 * k + 1)) * fs,
-                                   qh[k], qlo[k]);
+                    for (int k = 0; k < 4; ++k) split_hilo(v[word_value(2 * k)] * fs, v[word_value(2 * k + 1)] * fs, qh[k], qlo[k]);
                     const uint32_t at = sw128_byte(r, 2 * (col0 + i), 128);
                     *reinterpret_cast<uint4*>(sq + at) = make_uint4(qh[0], qh[1], qh[2], qh[3]);
                     if constexpr (QL == 2) *reinterpret_cast<uint4*>(sq + C::kQ + at) = make_uint4(qlo[0], qlo[1], qlo[2], qlo[3]);
@@ -528,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             // groups with a non-finite pair on a token that this row sees
             uint32_t bad = 0;
 #pragma unroll
-            for (int g = 0; g < NG; ++g) bad |= (uint32_t)(sBad[4 * (seg & 3) + g] < lim) << g;
+            for (int g = 0; g < NG; ++g) bad |= (uint32_t)(sBad[4 * (seg & 7) + g] < lim) << g;
             if (lsum != lsum && mref == -INFINITY) mref = 0.f;   // nothing but NaN scores
             if constexpr (MT == 1) {
                 xch[x * 128 + r] = mref;
@@ -546,34 +552,31 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 l1 = xch[3 * 128 + r];
             }
             const float mm = failed ? -INFINITY : fmaxf(m0, m1);
-            const float f0 = m0 == -INFINITY ? 0.f : fast_exp2(m0 - mm), f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - mm);
+            const float f0 = m0 == -INFINITY || failed ? 0.f : fast_exp2(m0 - mm);
+            const float f1 = m1 == -INFINITY || failed ? 0.f : fast_exp2(m1 - mm);
             const float L = mm == -INFINITY ? 0.f : (f0 == 0.f ? 0.f : f0 * l0) + (f1 == 0.f ? 0.f : f1 * l1);
             const float inv = whole && mm != -INFINITY ? 1.f / L : 1.f;
+            float* part = a.part_acc + (slot - ur) * D + ur;   // [D][ROWS]: the lanes of a store are neighbours
 #pragma unroll 1
-            for (int c0 = 0; c0 < kCols; c0 += 16) {
+            for (int c0 = 0; c0 < kCols; c0 += 8) {
                 const int col = col0 + c0;
-                uint32_t o0[16], o1[16];
-                tc_ld16(tl + C::kO + (MT == 2 ? D * x : 0) + col, o0);
-                if constexpr (MT == 1) tc_ld16(tl + C::kO + D + col, o1);
-                const bool poison = (bad >> (col / GRP)) & 1u; // (a run of 16 lies in one group)
+                uint32_t o0[8], o1[8];
+                tc_ld8(tl + C::kO + (MT == 2 ? D * x : 0) + col, o0);
+                if constexpr (MT == 1) tc_ld8(tl + C::kO + D + col, o1);
+                const bool poison = (bad >> (col / GRP)) & 1u; // (a run of 8 lies in one group)
                 if (!rvalid) continue;
-                float v[16];
+                float v[8];
 #pragma unroll
-                for (int cc = 0; cc < 16; ++cc) {
-                    float y = 0.f;
-                    if (mm != -INFINITY) {
-                        if (f0 != 0.f) y = __uint_as_float(o0[cc]) * f0;
-                        if constexpr (MT == 1)
-                            if (f1 != 0.f) y = fmaf(__uint_as_float(o1[cc]), f1, y);
-                        if (poison) y = __uint_as_float(0x7fc00000u);
-                    }
-                    v[(cc & ~7) + word_value(cc & 7)] = y * inv;
+                for (int cc = 0; cc < 8; ++cc) {
+                    float y = f0 != 0.f ? __uint_as_float(o0[cc]) * f0 : 0.f;
+                    if constexpr (MT == 1) y = f1 != 0.f ? fmaf(__uint_as_float(o1[cc]), f1, y) : y;
+                    v[word_value(cc)] = poison && mm != -INFINITY ? __uint_as_float(0x7fc00000u) : y * inv;
                 }
+                if (whole) {
+                    store8<DT>(a.out, qrow * D + col, a.vec16, v);
+                } else {
 #pragma unroll
-                for (int i = 0; i < 16; i += 8) {
-                    const float u[8] = {v[i], v[i + 1], v[i + 2], v[i + 3], v[i + 4], v[i + 5], v[i + 6], v[i + 7]};
-                    if (whole) store8<DT>(a.out, qrow * D + col + i, a.vec16, u);
-                    else store8<TQ_F32>(a.part_acc, slot * D + col + i, true, u);
+                    for (int e = 0; e < 8; ++e) part[(int64_t)(col + e) * ROWS] = v[e];
                 }
             }
             if (rvalid && !whole && (MT == 2 || x == 0)) {
@@ -586,8 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 a.split[c] = make_int4(w.b, w.rt * (int)a.Hkv + w.kv, (int)((end * nC - 1) / N), 1);
             }
             // the next segment's queries and exchange overwrite what was read here (the marks of
-            // this segment's slot are next used four segments on; producers are at most three ahead)
-            if (tid < 4) sBad[4 * (seg & 3) + tid] = INT_MAX;
+            // this segment's slot are next used eight segments on; producers are at most kBufs ahead)
+            if (tid < 4) sBad[4 * (seg & 7) + tid] = INT_MAX;
             tc_fence_before();
             soft_or(false);
             tc_fence_after();
@@ -636,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 for (int it = 0; it < 2 * kItems; ++it) {
                     if (it >= kItems && ((bits[it] & 0x7c00u) == 0x7c00u || (bits[it] & 0x7c000000u) == 0x7c000000u)) {
                         bits[it] = 0u;
-                        atomicMin(&sBad[4 * (seg & 3) + gam], (int)tok0 + tau0 + 32 * (it % kItems));
+                        atomicMin(&sBad[4 * (seg & 7) + gam], (int)tok0 + tau0 + 32 * (it % kItems));
                     }
                     // the largest value stays finite in fp16
                     if (fmaf(15.f, __low2float(as_h2(bits[it])), __high2float(as_h2(bits[it]))) > 65504.f) bits[it] -= 1u;
@@ -813,7 +816,7 @@ cudaError_t launch_t(const Int4AttendArgs& a, int num_sms, cudaStream_t s) {
         e = cudaGetLastError();
     }
     if (e != cudaSuccess) return e;
-    return launch_int4_combine<D, DT>(a, 128 * MT, true, ctas, s);
+    return launch_int4_combine_tiles<D, DT, MT>(a, ctas, s);
 }
 template <int D, int GRP>
 cudaError_t launch_g(tq_dtype dt, const Int4AttendArgs& a, int num_sms, cudaStream_t s) {
