@@ -221,36 +221,34 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// eight consecutive elements of a row (zeros where there is no row); vec: 16-byte aligned
-template <int DT>
-__device__ __forceinline__ void load8(const void* p, int64_t at, bool vec, bool there, float (&v)[8]) {
-    constexpr int kE = DT == TQ_F32 ? 4 : 2;
-    uint32_t w[2 * kE];
+// N consecutive elements of a row as stored (zeros where there is no row); vec: the row is 16-byte aligned
+template <int DT, int N>
+__device__ __forceinline__ void load_raw(const void* p, int64_t at, bool vec, bool there, uint32_t (&w)[N * (DT == TQ_F32 ? 4 : 2) / 4]) {
+    constexpr int kE = DT == TQ_F32 ? 4 : 2, kN = N * kE / 4;
 #pragma unroll
-    for (int i = 0; i < 2 * kE; ++i) w[i] = 0u;
+    for (int i = 0; i < kN; ++i) w[i] = 0u;
+    if (!there) return;
     const char* s = static_cast<const char*>(p) + at * kE;
-    if (there && vec) {
+    if (vec) {
 #pragma unroll
-        for (int i = 0; i < kE / 2; ++i) {
+        for (int i = 0; i < kN / 4; ++i) {
             const uint4 u = __ldg(reinterpret_cast<const uint4*>(s) + i);
             w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
         }
-    } else if (there) {
-        if constexpr (DT == TQ_F32) {
+    } else if constexpr (DT == TQ_F32) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = reinterpret_cast<const uint32_t*>(s)[i];
-        } else {
-            const uint16_t* h = reinterpret_cast<const uint16_t*>(s);
+        for (int i = 0; i < kN; ++i) w[i] = reinterpret_cast<const uint32_t*>(s)[i];
+    } else {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(s);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = (uint32_t)h[2 * i] | ((uint32_t)h[2 * i + 1] << 16);
-        }
+        for (int i = 0; i < kN; ++i) w[i] = (uint32_t)h[2 * i] | ((uint32_t)h[2 * i + 1] << 16);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if constexpr (DT == TQ_F32) v[i] = __uint_as_float(w[i]);
-        else if constexpr (DT == TQ_BF16) v[i] = __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
-        else v[i] = (i & 1) ? __high2float(as_h2(w[i >> 1])) : __low2float(as_h2(w[i >> 1]));
-    }
+}
+template <int DT, int N>
+__device__ __forceinline__ float raw_elem(const uint32_t (&w)[N], int e) {
+    if constexpr (DT == TQ_F32) return __uint_as_float(w[e]);
+    else if constexpr (DT == TQ_BF16) return __uint_as_float((e & 1) ? w[e >> 1] & 0xffff0000u : w[e >> 1] << 16);
+    else return (e & 1) ? __high2float(as_h2(w[e >> 1])) : __low2float(as_h2(w[e >> 1]));
 }
 // eight consecutive outputs
 template <int DT>
@@ -406,16 +404,13 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             // position p of a word's eight holds value word_value(p), as in the expanded operands
             float fr;
             {
-                // (two passes over the row, the second from the cache, in short loops: a unit's start and end
-                // run once per unit and are bound by fetching their instructions)
+                // (all loads at once; 64 registers with MT = 2)
+                constexpr int kRegs = kCols * (DT == TQ_F32 ? 4 : 2) / 4;
+                uint32_t raw_q[kRegs];
+                load_raw<DT, kCols>(a.q, qrow * D + col0, a.vec16, rvalid, raw_q);
                 float mx = 0.f;
-#pragma unroll 4
-                for (int i = 0; i < kCols; i += 8) {
-                    float v[8];
-                    load8<DT>(a.q, qrow * D + col0 + i, a.vec16, rvalid, v);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(v[e]));
-                }
+                for (int e = 0; e < kCols; ++e) mx = fmaxf(mx, fabsf(raw_elem<DT>(raw_q, e)));
                 if constexpr (MT == 1) {
                     xch[x * 128 + r] = mx;
                     soft_or(false);
@@ -427,13 +422,13 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 const float fs = a.scale_log2 < 0.f ? -f : f;
                 fr = fmaxf(fabsf(a.scale_log2) / f, 1e-37f);  // (above zero: a masked -inf stays one)
                 uint8_t* sq = sm + C::kOffQ + (MT == 2 ? x * QL * C::kQ : 0);
-#pragma unroll 2
+#pragma unroll
                 for (int i = 0; i < kCols; i += 8) {           // eight positions, 16 bytes
-                    float v[8];
-                    load8<DT>(a.q, qrow * D + col0 + i, a.vec16, rvalid, v);
                     uint32_t qh[4], qlo[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) split_hilo(v[word_value(2 * k)] * fs, v[word_value(2 * k + 1)] * fs, qh[k], qlo[k]);
+                    for (int k = 0; k < 4; ++k)
+                        split_hilo(raw_elem<DT>(raw_q, i + word_value(2 * k)) * fs, raw_elem<DT>(raw_q, i + word_value(2 * k + 1)) * fs,
+                                   qh[k], qlo[k]);
                     const uint32_t at = sw128_byte(r, 2 * (col0 + i), 128);
                     *reinterpret_cast<uint4*>(sq + at) = make_uint4(qh[0], qh[1], qh[2], qh[3]);
                     if constexpr (QL == 2) *reinterpret_cast<uint4*>(sq + C::kQ + at) = make_uint4(qlo[0], qlo[1], qlo[2], qlo[3]);
