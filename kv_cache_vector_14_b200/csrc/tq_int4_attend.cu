@@ -16,7 +16,8 @@
 //     limbs of its own head.
 //   * A value nibble c in the low mantissa bits of an fp16 is the subnormal number
 //     c 2^-24 (16 c 2^-24 one nibble higher), which the tensor core multiplies
-//     exactly: one AND per pair and one shift per four pairs, no conversion.  A
+//     exactly: one AND per pair and one shift per four pairs, no conversion (fp32
+//     calls spend two more, see pick).  A
 //     transposing shared-memory load brings the nibbles of two tokens into one
 //     register.  The softmax weights times the value scales, p vs, are the other
 //     operand: fp16 hi and lo limbs in two columns (22 bits), for bf16 outputs hi
@@ -81,10 +82,12 @@ struct Shape {
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
-constexpr float kTwo24 = 16777216.f;
 constexpr float kHuge = 3.4e38f;
-constexpr float kRoom = 7.f;      // p vs is kept below 2^(kRoom + kLazy) = 2^15 (fp16 holds 65504) ...
-constexpr float kLazy = 8.f;      // ... and the reference exponent moves only when it is exceeded by this much
+// p vs is kept below 2^(room + lazy) = 2^15 (fp16 holds 65504), and the reference exponent moves only
+// when 2^room is exceeded by 2^lazy.  Two limbs want the room: the low limb of a weight below 2^-3 is
+// subnormal.
+__host__ __device__ constexpr float room(bool one_limb) { return one_limb ? 7.f : 13.f; }
+__host__ __device__ constexpr float lazy(bool one_limb) { return 15.f - room(one_limb); }
 
 template <int DT>
 __device__ __forceinline__ float load_elem(const void* p, int64_t i) {
@@ -164,14 +167,22 @@ __device__ __forceinline__ void imma_u8s8(int (&d)[4], const uint32_t (&a)[4], u
         : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// nibble R of both halves of x as fp16 subnormals (c 2^-24 for even R, 16 c 2^-24 for odd), the
-// high half's as 15 - c: (x & mask) ^ flip in one instruction; x8 = x >> 8
-template <int R>
+// nibble R of both halves of x as fp16, the high half's as 15 - c; x8 = x >> 8.  EXACT = false: the
+// subnormals c 2^-24 (16 c 2^-24 for odd R), (x & mask) ^ flip in one instruction.  The tensor core
+// multiplies them exactly, but aligns its sums by the exponent field, which for a subnormal stands 7
+// to 10 bits above the value, so those bits are lost from the sum: 5e-6 of the result.  EXACT = true
+// (fp32 calls): c (16 c) as a normal number, two instructions more.
+template <int R, bool EXACT>
 __device__ __forceinline__ uint32_t pick(uint32_t x, uint32_t x8) {
     uint32_t r;
     asm("lop3.b32 %0, %1, %2, %3, 0x6a;"
         : "=r"(r)
         : "r"(R < 2 ? x : x8), "r"((R & 1) ? 0x00f000f0u : 0x000f000fu), "r"((R & 1) ? 0x00f00000u : 0x000f0000u));
+    if constexpr (EXACT) {
+        r |= 0x64006400u;                                     // 1024 + c
+        const uint32_t m1024 = 0xe400e400u;
+        r = h2_bits(__hadd2(*reinterpret_cast<const __half2*>(&r), *reinterpret_cast<const __half2*>(&m1024)));
+    }
     return r;
 }
 // v as four signed byte digits, v = l0 + 256 l1 + 65536 l2 + 2^24 l3 (adding 128 to each of the
@@ -203,6 +214,8 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
     // bf16 outputs: weights as one fp16 limb, columns (head t, head 4 + t); else (hi, lo) of head t per n-tile
     constexpr bool kOneLimb = DT == TQ_BF16;
     constexpr int VT = kOneLimb ? 1 : NT;                     // value n-tiles
+    constexpr float kRoom = room(kOneLimb), kLazy = lazy(kOneLimb);
+    constexpr float kUnit = DT == TQ_F32 ? 1.f : 16777216.f;  // what one of a value operand's code stands for (see pick)
     constexpr bool kFragSmem = D == 256;
     extern __shared__ __align__(128) uint8_t smem[];
     float* sAcc = reinterpret_cast<float*>(smem + S::kOffAcc);
@@ -660,8 +673,8 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
                             }
                             // registers: tokens 2t, 2t + 1 (low, high half) and 8 further on, values 32 c + 4 g ..
                             const uint32_t x = v4[2 * h], y = v4[2 * h + 1], x8 = x >> 8, y8 = y >> 8;
-                            const uint32_t va[4] = {pick<0>(x, x8), pick<1>(x, x8), pick<0>(y, y8), pick<1>(y, y8)};
-                            const uint32_t vb[4] = {pick<2>(x, x8), pick<3>(x, x8), pick<2>(y, y8), pick<3>(y, y8)};
+                            const uint32_t va[4] = {pick<0, DT == TQ_F32>(x, x8), pick<1, DT == TQ_F32>(x, x8), pick<0, DT == TQ_F32>(y, y8), pick<1, DT == TQ_F32>(y, y8)};
+                            const uint32_t vb[4] = {pick<2, DT == TQ_F32>(x, x8), pick<3, DT == TQ_F32>(x, x8), pick<2, DT == TQ_F32>(y, y8), pick<3, DT == TQ_F32>(y, y8)};
 #pragma unroll
                             for (int vt = 0; vt < VT; ++vt) {
                                 mma16816(o[vt][2 * c], va, pb[vt][0], pb[vt][1]);
@@ -715,8 +728,8 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
                     const int gam = 16 * mt / GRP, val = 32 * (mt >> 1) + 4 * gr + 2 * (mt & 1);
                     const float x = kOneLimb ? o[0][mt][nt] : o[kOneLimb ? 0 : nt][mt][0] + o[kOneLimb ? 0 : nt][mt][1];
                     const float y = kOneLimb ? o[0][mt][2 + nt] : o[kOneLimb ? 0 : nt][mt][2] + o[kOneLimb ? 0 : nt][mt][3];
-                    dst[val] = fmaf(x, kTwo24, oz[nt][gam]);
-                    dst[val + 1] = fmaf(y, kTwo24 / 16.f, oz[nt][gam]);
+                    dst[val] = fmaf(x, kUnit, oz[nt][gam]);
+                    dst[val + 1] = fmaf(y, kUnit / 16.f, oz[nt][gam]);
                 }
             }
         }

@@ -23,7 +23,7 @@
 // the values of this one, so that softmax and tensor core overlap.  The mma of one
 // thread run in issue order, so a score buffer is not overwritten before the product
 // with the weights in it has run.  The reference exponent moves only when it is
-// exceeded by 2^8; then O is rescaled, once the stream's last product is done.
+// exceeded by 2^8 (two limbs: 2^2); then O is rescaled, once the stream's last product is done.
 //
 // Work: the units' tiles (each unit only as far as its last row sees) laid end
 // to end, shared out evenly over one CTA per SM on the device, cut units merged
@@ -47,8 +47,6 @@ constexpr int kSoft = 256;                // softmax threads: two streams x 128 
 constexpr int kProd = 128;                // producer threads
 constexpr int kThreads = kSoft + kProd + 64;
 constexpr int kSlots = 3;                 // ring of raw tiles (a K and a V block)
-constexpr float kRoom = 7.f, kLazy = 8.f; // P is kept below 2^15 (fp16 holds 65504)
-
 template <int D, int GRP, int NL, int QL, int MT>
 struct Ch {
     static constexpr int kNG = D / GRP;
@@ -280,6 +278,8 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
     constexpr int NL = DT == TQ_BF16 ? 1 : 2;                 // limbs of K, V and P
     constexpr int QL = DT == TQ_F32 ? 2 : 1;                  // limbs of Q
     constexpr int ROWS = 128 * MT;
+    // P is kept below 2^15 (fp16 holds 65504); two limbs need the room (see tq_int4_attend.cu)
+    constexpr float kRoom = NL == 1 ? 7.f : 13.f, kLazy = 15.f - kRoom;
     using C = Ch<D, GRP, NL, QL, MT>;
     constexpr int NG = C::kNG, TT = C::TT;
     using W = Walk<ROWS, TT>;
