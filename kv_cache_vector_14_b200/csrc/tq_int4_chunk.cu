@@ -67,6 +67,10 @@ struct Ch {
     static_assert(kOffRing % 16 == 0 && kOffBar % 8 == 0 && kOffScan % 8 == 0, "alignment");
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
     // tensor memory columns
+    // Tiles of a segment.  The tensor core truncates its sums, and 12 additions per tile onto an fp32
+    // O cost an fp32 call 3e-5 of its result in 225 tiles; so O is taken out every 16 of a stream's tiles and added
+    // up in the workspace, correctly rounded.  (16-bit outputs do not show it.)
+    static constexpr int kSegTiles = QL == 1 ? INT_MAX / 2 : MT == 2 ? 16 : 32;
     static constexpr int kX = 0;                              // S / P of stream x, buffer b at TT (2 x + b)
     static constexpr int kO = 4 * TT;                         // O of stream x at kO + D x
     static_assert(kO + 2 * D <= 512, "tensor memory");
@@ -387,10 +391,14 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
         const int col0 = MT == 2 ? 0 : x * kCols;
         W w = w0;
         int seg = 0, nS = 0;                                  // segments, S of this stream so far
+        bool cont = false, ubegins = false;                   // the unit has a part in the workspace; it begins in this CTA
+        float fr = 0.f, mrun = -INFINITY, lrun = 0.f;         // its score factor, and that part's reference and sum
         for (int j = 0; j < J; ++seg) {
             // ---- a segment: tiles j .. j1 - 1 of one unit
             const int k0 = w.k, left = w.nt - w.k;
-            const int j1 = j + left < J ? j + left : J;
+            const int most = left < C::kSegTiles ? left : C::kSegTiles;
+            const int j1 = j + most < J ? j + most : J;
+            if (QL == 1 || !cont) ubegins = k0 == 0;
             const int ur = MT == 2 ? 128 * x + r : r;         // row of the unit
             const int64_t grow = (int64_t)w.rt * ROWS + ur;
             const bool rvalid = grow < a.rows;
@@ -402,8 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             const int lim = lim64 < 0 ? 0 : (int)lim64;
             // query operand: the row scaled by a power of two (largest element in [2^14, 2^15));
             // position p of a word's eight holds value word_value(p), as in the expanded operands
-            float fr;
-            {
+            if (QL == 1 || !cont) {
                 // (all loads at once; 64 registers with MT = 2)
                 constexpr int kRegs = kCols * (DT == TQ_F32 ? 4 : 2) / 4;
                 uint32_t raw_q[kRegs];
@@ -434,8 +441,8 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                     if constexpr (QL == 2) *reinterpret_cast<uint4*>(sq + C::kQ + at) = make_uint4(qlo[0], qlo[1], qlo[2], qlo[3]);
                 }
                 fence_proxy_async();
-                mbar_arrive(bar(kBarQ));
             }
+            mbar_arrive(bar(kBarQ));
             float mref = -INFINITY, lsum = 0.f;
             bool any = false;                                  // this stream has an O
             const bool idle = !__any_sync(kFull, rvalid);      // none of the warp's rows is there
@@ -536,8 +543,8 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 xch[(2 + x) * 128 + r] = lsum;
             }
             if (soft_or(failed)) failed = true;
-            const bool begins = k0 == 0, ends = j1 - j == left, whole = begins && ends;
-            const int64_t slot = (2 * c + (begins ? 1 : 0)) * ROWS + ur;
+            const bool ends = j1 - j == left, whole = ubegins && ends;
+            const int64_t slot = (2 * c + (ubegins ? 1 : 0)) * ROWS + ur;
             // MT = 1: both streams' results, each stream half of the coordinates
             float m0 = mref, m1 = -INFINITY, l0 = lsum, l1 = 0.f;
             if constexpr (MT == 1) {
@@ -546,10 +553,15 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 l0 = xch[2 * 128 + r];
                 l1 = xch[3 * 128 + r];
             }
-            const float mm = failed ? -INFINITY : fmaxf(m0, m1);
+            if (!cont) { mrun = -INFINITY; lrun = 0.f; }
+            const float mm = failed ? -INFINITY : fmaxf(fmaxf(m0, m1), mrun);
             const float f0 = m0 == -INFINITY || failed ? 0.f : fast_exp2(m0 - mm);
             const float f1 = m1 == -INFINITY || failed ? 0.f : fast_exp2(m1 - mm);
-            const float L = mm == -INFINITY ? 0.f : (f0 == 0.f ? 0.f : f0 * l0) + (f1 == 0.f ? 0.f : f1 * l1);
+            const float f2 = mrun == -INFINITY || failed ? 0.f : fast_exp2(mrun - mm);
+            float L = f2 * lrun;
+            if (f0 != 0.f) L = fmaf(f0, l0, L);
+            if (f1 != 0.f) L = fmaf(f1, l1, L);
+            if (mm == -INFINITY) L = 0.f;
             const float inv = whole && mm != -INFINITY ? 1.f / L : 1.f;
             float* part = a.part_acc + (slot - ur) * D + ur;   // [D][ROWS]: the lanes of a store are neighbours
 #pragma unroll 1
@@ -565,8 +577,14 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 for (int cc = 0; cc < 8; ++cc) {
                     float y = f0 != 0.f ? __uint_as_float(o0[cc]) * f0 : 0.f;
                     if constexpr (MT == 1) y = f1 != 0.f ? fmaf(__uint_as_float(o1[cc]), f1, y) : y;
-                    v[word_value(cc)] = poison && mm != -INFINITY ? __uint_as_float(0x7fc00000u) : y * inv;
+                    v[word_value(cc)] = poison && mm != -INFINITY ? __uint_as_float(0x7fc00000u) : y;
                 }
+                if (QL == 2 && cont) {                         // what this thread stored there (0 NaN stays NaN)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] = fmaf(part[(int64_t)(col + e) * ROWS], f2, v[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] *= inv;
                 if (whole) {
                     store8<DT>(a.out, qrow * D + col, a.vec16, v);
                 } else {
@@ -578,8 +596,8 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 a.part_ml[2 * slot] = mm;
                 a.part_ml[2 * slot + 1] = L;
             }
-            // a unit that begins here and goes on: up to the CTA of its last tile
-            if (tid == 0 && begins && !ends) {
+            // a unit that begins here and goes on behind this CTA: up to the CTA of its last tile
+            if (tid == 0 && ubegins && !ends && j1 == J) {
                 const int64_t end = lo + j + left;             // (flattened index behind its last tile)
                 a.split[c] = make_int4(w.b, w.rt * (int)a.Hkv + w.kv, (int)((end * nC - 1) / N), 1);
             }
@@ -589,7 +607,12 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             tc_fence_before();
             soft_or(false);
             tc_fence_after();
-            w.k = w.nt - 1;                                    // on to the next unit
+            if constexpr (QL == 2) {
+                cont = !ends;
+                mrun = mm;
+                lrun = L;
+            }
+            w.k += j1 - j - 1;                                 // on to the next segment
             w.next(a);
             j = j1;
         }
@@ -608,7 +631,8 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
 #pragma unroll
         for (int i = 0; i < 4; ++i) at[i] = sw128_byte(tau0, 2 * (32 * cp + 8 * i), TT);
         // (no warp-collective instruction here: a thread whose wait runs out leaves, the others follow)
-        int slot = 0, sp = 0, bf = 0, bfp = 0, seg = 0;        // ring slot and buffer, with their phases
+        int slot = 0, sp = 0, bf = 0, bfp = 0;                 // ring slot and buffer, with their phases
+        int seg = 0, inseg = 0;                                // segment, tiles of it
         for (int j = 0; j < J; ++j) {
             if (!mbar_wait_bounded(bar(kBarRing + slot), (uint32_t)sp)) { failed = true; break; }
             const uint8_t* raw_blk = sm + C::kOffRing + slot * 2 * C::kBlockB;
@@ -659,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             mbar_arrive(bar(kBarSlot + slot));
             if (++slot == kSlots) { slot = 0; sp ^= 1; }
             if (++bf == C::kBufs) { bf = 0; bfp ^= 1; }
-            if (w.k == w.nt - 1) ++seg;
+            if (++inseg == C::kSegTiles || w.k == w.nt - 1) { ++seg; inseg = 0; }
             w.next(a);
         }
         if (failed) atomicExch(a.err, 1);
@@ -711,7 +735,8 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             const uint32_t xd = tmem + C::kX + TT * b;
             uint32_t acc = 0u;
 #pragma unroll
-            for (int pr = 0; pr < 3; ++pr) {                   // hi hi, lo hi, hi lo
+            for (int q = 1; q <= 3; ++q) {                     // lo hi, hi lo, hi hi: the small ones first (truncated sums)
+                const int pr = q % 3;
                 if ((pr == 1 && QL == 1) || (pr == 2 && NL == 1)) continue;
                 const uint32_t ql = pr == 1 ? (uint32_t)C::kQ : 0u, kl = pr == 2 ? (uint32_t)C::kTile : 0u;
 #pragma unroll
@@ -763,7 +788,8 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
         };
         int vb = 0;                        // buffer of the next values (its scores have waited for it)
         for (int j = 0, seg = 0; j < J && ok; ++seg) {
-            const int left = w.nt - w.k, j1 = j + left < J ? j + left : J;     // the segment's tiles
+            const int left = w.nt - w.k, most = left < C::kSegTiles ? left : C::kSegTiles;
+            const int j1 = j + most < J ? j + most : J;        // the segment's tiles
             if (!(ok = warp_wait(bar(kBarQ), (uint32_t)(seg & 1)))) break;
             for (int i = 0; i < kAhead && j + i < j1 && ok; ++i) ok = scores(j + i);
             for (int i = j; i < j1 && ok; ++i) {
@@ -780,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 commit(bar(kBarSeg));
                 if (lane == 0) mbar_arrive(bar(kBarSeg));      // (orders what the producers noted, seen through their arrivals)
             }
-            w.k = w.nt - 1;
+            w.k += j1 - j - 1;
             w.next(a);
             j = j1;
         }

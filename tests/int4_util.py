@@ -67,13 +67,14 @@ def read_cache(raw, d, group, blocks, T):
     return codes, pairs[..., 0], pairs[..., 1]
 
 
-def attend(q, k, v, scale, n_q):
-    """q [Lq, d], k, v [T, d] float64; query i sees tokens [0, T - Lq + 1 + i).  Returns [Lq, d]."""
+def attend(q, k, v, scale, n_q, every=None):
+    """q [Lq, d], k, v [T, d] float64; query i sees tokens [0, T - Lq + 1 + i).  Returns [Lq, d] (every: only
+    each every-th query)."""
     T = len(k)
     out = np.zeros(q.shape)
     for i in range(n_q):
         n = T - n_q + 1 + i
-        if n <= 0:
+        if n <= 0 or (every and i % every):
             continue
         s = scale * (k[:n] @ q[i])
         p = np.exp(s - s.max())

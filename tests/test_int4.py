@@ -225,7 +225,7 @@ def test_positions_outside_the_cache_are_skipped_and_reported(libtq):
 # ------------------------------------------------------------------ attention
 
 def run_attend(d, group, dtype, G, Hkv, lens, Lq=1, paged=False, uniform=False, Tcap=None, seed=0, scale=None, qmul=1.0,
-               vmul=1.0):
+               vmul=1.0, lq_check=None):
     B = len(lens)
     Tcap = Tcap or max(64, -(-max(lens) // 64) * 64)
     cs = Case(d, group, B, Hkv, Tcap, paged, seed)
@@ -319,6 +319,13 @@ def test_chunks(libtq, d, group, dtype, G, Lq, lens):
                                              (1.0, 1.0, -0.2)])
 def test_chunk_magnitudes(libtq, dtype, qmul, vmul, scale):
     run_attend(128, 64, dtype, 4, 1, [700, 90], Lq=20, scale=scale, qmul=qmul, vmul=vmul, seed=3)
+
+
+@gpu
+@pytest.mark.parametrize("G,Lq,T,Hkv", [(1, 9, 9000, 2), (4, 60, 5000, 8), (2, 130, 3000, 5)])
+def test_chunk_fp32_sums_of_many_tiles(libtq, G, Lq, T, Hkv):
+    """fp32 chunks whose CTAs walk many tiles of one unit: the sums are taken out of the tensor core in between."""
+    run_attend(128, 64, "f32", G, Hkv, [T, T // 2], Lq=Lq, seed=G, lq_check=3)
 
 
 @gpu
