@@ -46,6 +46,7 @@ namespace {
 constexpr int kSoft = 256;                // softmax threads: two streams x 128 rows
 constexpr int kProd = 128;                // producer threads
 constexpr int kThreads = kSoft + kProd + 64;
+constexpr float kHuge = 3.40282347e38f;   // the largest finite fp32
 constexpr int kSlots = 3;                 // ring of raw tiles (a K and a V block)
 template <int D, int GRP, int NL, int QL, int MT>
 struct Ch {
@@ -417,17 +418,21 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 load_raw<DT, kCols>(a.q, qrow * D + col0, a.vec16, rvalid, raw_q);
                 float mx = 0.f;
 #pragma unroll
-                for (int e = 0; e < kCols; ++e) mx = fmaxf(mx, fabsf(raw_elem<DT>(raw_q, e)));
+                for (int e = 0; e < kCols; ++e) {
+                    const float v = fabsf(raw_elem<DT>(raw_q, e));
+                    mx = fmaxf(mx, v <= kHuge ? v : INFINITY); // (a NaN counts as infinite)
+                }
                 if constexpr (MT == 1) {
                     xch[x * 128 + r] = mx;
                     soft_or(false);
                     mx = fmaxf(mx, xch[(x ^ 1) * 128 + r]);
                 }
-                int ex = mx > 0.f ? ilogbf(mx) : 0;
+                int ex = mx > 0.f && mx <= kHuge ? ilogbf(mx) : 0;
                 ex = ex < -100 ? -100 : ex;
-                const float f = mx <= 3.4e38f ? exp2f((float)(14 - ex)) : 1.f;
+                const float f = mx <= kHuge ? exp2f((float)(14 - ex)) : 1.f;
                 const float fs = a.scale_log2 < 0.f ? -f : f;
-                fr = fmaxf(fabsf(a.scale_log2) / f, 1e-37f);  // (above zero: a masked -inf stays one)
+                // (above zero: a masked -inf stays one; a query with an infinity or a NaN makes its row NaN)
+                fr = mx <= kHuge ? fmaxf(fabsf(a.scale_log2) / f, 1e-37f) : __int_as_float(0x7fc00000);
                 uint8_t* sq = sm + C::kOffQ + (MT == 2 ? x * QL * C::kQ : 0);
 #pragma unroll
                 for (int i = 0; i < kCols; i += 8) {           // eight positions, 16 bytes

@@ -567,3 +567,103 @@ def test_refusals(libtq):
     with pytest.raises(tq.TQError):
         tq.tq_attend_int4(h, q, kc, tq.Int4Cache(d, group, 2, 2, 192), out, ws, T=10)
     cs.close()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_chunk_queries_that_are_not_finite(libtq, dtype):
+    """In a chunk too, a NaN or infinite query makes its own row NaN and no other."""
+    cs, _, _ = _filled(128, 64, 1, 1, 128, 5)
+    q = torch.randn((1, 50, 4, 128), device="cuda").to(TYPES[dtype])
+    q[0, 3, 1, 7], q[0, 20, 0, 100], q[0, 49, 3, 0] = float("nan"), float("inf"), float("-inf")
+    out = torch.zeros_like(q)
+    ws = torch.zeros(tq.tq_attend_int4_workspace_bytes(cs.h, 1, 50, 4, 1), dtype=torch.uint8, device="cuda")
+    tq.tq_attend_int4(cs.h, q, *cs.caches, out, ws, T=100, scale=0.1)
+    rows = torch.isnan(out).any(-1)[0]
+    assert torch.equal(rows, torch.isnan(out).all(-1)[0]) and int(rows.sum()) == 3
+    assert rows[3, 1] and rows[20, 0] and rows[49, 3]
+    cs.close()
+
+
+@gpu
+@pytest.mark.parametrize("Lq,dtype", [(1, "bf16"), (40, "bf16"), (40, "f32")])
+def test_queries_off_a_16_byte_boundary(libtq, Lq, dtype):
+    cs, _, rng = _filled(128, 64, 2, 2, 128, 8)
+    n = 2 * Lq * 8 * 128
+    q = to_gpu(rng.standard_normal(n).astype(np.float32), dtype).view(2, Lq, 8, 128)
+    flat = [torch.zeros(n + 1, dtype=q.dtype, device="cuda") for _ in range(2)]
+    q1, out1 = (f[1:].view(q.shape) for f in flat)
+    q1.copy_(q)
+    out = torch.zeros_like(q)
+    ws = torch.zeros(tq.tq_attend_int4_workspace_bytes(cs.h, 2, Lq, 8, 2), dtype=torch.uint8, device="cuda")
+    lens = torch.tensor([128, 60], dtype=torch.int32, device="cuda")
+    tq.tq_attend_int4(cs.h, q, *cs.caches, out, ws, seq_lens=lens, scale=0.1)
+    tq.tq_attend_int4(cs.h, q1, *cs.caches, out1, ws, seq_lens=lens, scale=0.1)
+    assert torch.equal(out, out1)
+    cs.close()
+
+
+@gpu
+def test_captured_chunk_replays_beside_another_graph(libtq):
+    """Two graphs of chunk steps that share one workspace, replayed in turn with new contents."""
+    d, group, B, Hkv, G, Lq = 128, 64, 2, 2, 4, 20
+    cs, _, rng = _filled(d, group, B, Hkv, 320, 3)
+    ws = torch.zeros(tq.tq_attend_int4_workspace_bytes(cs.h, B, Lq, Hkv * G, Hkv), dtype=torch.uint8, device="cuda")
+    ws2 = torch.zeros_like(ws)
+    q = [to_gpu(rng.standard_normal((B, Lq, Hkv * G, d)).astype(np.float32), "bf16") for _ in range(2)]
+    kv = [to_gpu(rand(rng, (B, Hkv, Lq, d)), "bf16") for _ in range(2)]
+    pos = [torch.tensor(p, dtype=torch.int32, device="cuda") for p in ([7, 200], [300, 0])]
+    out = [torch.zeros_like(x) for x in q]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    with torch.cuda.stream(side):
+        for i in range(2):
+            g = torch.cuda.CUDAGraph()
+            tq.tq_append_attend_int4(cs.h, kv[0], kv[1], *cs.caches, q[i], out[i], ws, pos=pos[i], scale=0.1)
+            with torch.cuda.graph(g, stream=side):
+                tq.tq_append_attend_int4(cs.h, kv[0], kv[1], *cs.caches, q[i], out[i], ws, pos=pos[i], scale=0.1)
+            graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for x in kv + q:
+            x.copy_(torch.randn_like(x.float()).to(x.dtype))
+        for i in range(2):
+            graphs[i].replay()
+            torch.cuda.synchronize()
+            ref = torch.zeros_like(q[i])
+            tq.tq_attend_int4(cs.h, q[i], *cs.caches, ref, ws2, seq_lens=pos[i] + Lq, scale=0.1)
+            assert torch.equal(out[i], ref)
+    cs.close()
+
+
+@gpu
+@pytest.mark.parametrize("Lq", [1, 20])
+def test_offsets_beyond_32_bits(libtq, Lq):
+    """A pool of more than 4 GiB, its last pages in use."""
+    d, group, n = 128, 64, 960000
+    bb = tq.tq_int4_block_bytes(d, group)
+    assert n * bb > 1 << 32
+    h = tq.tq_init(d, 0)
+    pool = torch.empty(n * bb, dtype=torch.uint8, device="cuda")
+    far = torch.arange(n - 4, n, dtype=torch.int32, device="cuda").view(2, 2)
+    near = torch.arange(4, dtype=torch.int32, device="cuda").view(2, 2)
+    caches = [[tq.Int4Cache(d, group, 1, 2, 128, buf=pool[:n * bb], block_table=t, pool_blocks=n) for t in ((t_, t_))]
+              for t_ in (far, near + 4)]
+    x = torch.randn((1, 2, 128, d), device="cuda")
+    q = torch.randn((1, Lq, 8, d), device="cuda")
+    ws = torch.zeros(tq.tq_attend_int4_workspace_bytes(h, 1, Lq, 8, 2), dtype=torch.uint8, device="cuda")
+    outs, back = [], []
+    for kc, vc in caches:
+        tq.tq_encode_int4(h, x, kc)
+        out, b = torch.zeros_like(q), torch.zeros_like(x)
+        tq.tq_attend_int4(h, q, kc, vc, out, ws, T=120, scale=0.1)
+        tq.tq_expand_int4(h, kc, b)
+        outs.append(out)
+        back.append(b)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(back[0], back[1]) and outs[0].abs().sum() > 0
+    pg = tq.Pages(far, torch.zeros(n, dtype=torch.int32, device="cuda"), 2, [(pool, bb)])
+    tq.tq_pages_copy(h, pg, pg, far.view(-1), torch.arange(100, 104, dtype=torch.int32, device="cuda"))
+    assert torch.equal(pool[100 * bb:104 * bb], pool[(n - 4) * bb:])
+    assert tq.tq_device_status(h) == tq.TQ_OK
+    tq.tq_destroy(h)
