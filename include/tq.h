@@ -329,8 +329,8 @@ TQ_API tq_status tq_encode_int4(const tq_handle* h, int group, const void* x, tq
 
 /* Read T tokens per (batch, kv head) back as values of `dtype` (fp32 value
  * zero + scale * code rounded once); positions as tq_encode_int4, x is the
- * output with its strides.  Vectors of skipped positions are left as they
- * were.  Errors: as tq_encode_int4. */
+ * output with its strides (no two vectors on the same bytes).  Vectors of
+ * skipped positions are left as they were.  Errors: as tq_encode_int4. */
 TQ_API tq_status tq_expand_int4(const tq_handle* h, int group, void* x, tq_dtype dtype, int64_t B, int64_t Hkv,
                                 int64_t T, int64_t sb, int64_t sh, int64_t st, const tq_cache* c, const int32_t* pos,
                                 int64_t t0, void* stream);
@@ -369,7 +369,8 @@ TQ_API tq_status tq_attend_int4(const tq_handle* h, int group, const void* q, tq
  * with their Lq queries over the pos[b] + Lq tokens.  Results are those of
  * tq_encode_int4 on both caches and tq_attend_int4 with seq_lens = pos + Lq.
  * k_new and v_new share kv_dtype and strides.  The encodes are one launch, and
- * the attention's set-up overlaps it.  kc and vc must not overlap.
+ * the attention's set-up overlaps it.  kc and vc must not share blocks
+ * (contiguous caches that overlap, or one pool under one table, are refused).
  * Errors: those of tq_encode_int4 and tq_attend_int4, before any launch. */
 TQ_API tq_status tq_append_attend_int4(const tq_handle* h, int group, const void* k_new, const void* v_new,
                                        tq_dtype kv_dtype, int64_t Lq, int64_t sb, int64_t sh, int64_t st,
@@ -390,8 +391,8 @@ TQ_API tq_status tq_append_attend_int4(const tq_handle* h, int group, const void
  * layer or of several that share the table.  The same block_table goes into
  * the tq_cache of each.  A cache whose pages are shared (refs > 1) must not be
  * written there: tq_pages_alloc gives the writer its own copy first.
- * Entries outside [-1, pool_blocks) are left alone and reported by
- * tq_device_status, as are indices out of range.  Calls enqueue kernels, do
+ * Any negative entry counts as -1.  Entries of pool_blocks or more are left
+ * alone and reported by tq_device_status, as are indices out of range.  Calls enqueue kernels, do
  * not synchronise, and their outcome does not depend on thread order.  One
  * call at a time may work on a state. */
 #define TQ_MAX_PAGE_BUFFERS 128

@@ -89,6 +89,15 @@ cudaError_t launch_any(const tq_handle* h, int group, tq_dtype dt, const Int4Att
                                                 : launch_int4_attend(h->d, group, dt, a, h->num_sms, s);
 }
 
+// Whether tokens of the two caches may share blocks: contiguous ones whose bytes meet, or one pool
+// under one table (two tables over one pool are taken to name different blocks).
+bool caches_meet(const tq_handle* h, int group, const tq_cache* x, const tq_cache* y) {
+    if (x->block_table || y->block_table) return x->base == y->base && x->block_table == y->block_table;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x->base), b = reinterpret_cast<uintptr_t>(y->base);
+    const uintptr_t n = (uintptr_t)(x->B * x->Hkv * (x->Tcap / kBlockT) * int4_block_bytes(h->d, group));
+    return a < b + n && b < a + n;                     // (of one size: prepare_attend)
+}
+
 // Checks of an attention call and its kernel arguments; *empty: nothing to do.
 tq_status prepare_attend(const tq_handle* h, int group, const void* q, tq_dtype qdt, int64_t B, int64_t Lq, int64_t Hq,
                          const tq_cache* kc, const tq_cache* vc, const int32_t* lens, int64_t T, int64_t add, float scale,
@@ -97,7 +106,7 @@ tq_status prepare_attend(const tq_handle* h, int group, const void* q, tq_dtype 
     if (!h || !dtype_ok(qdt) || !cache_ok(h, kc) || !cache_ok(h, vc) || !int4_group_ok(h->d, group))
         return TQ_ERR_INVALID_ARG;
     if (B < 0 || Lq < 0 || Hq <= 0 || kc->B != B || vc->B != B || kc->Hkv != vc->Hkv || kc->Tcap != vc->Tcap ||
-        Hq % kc->Hkv || !std::isfinite(scale) || (lens && !aligned(lens, 4)))
+        Hq % kc->Hkv || !std::isfinite(scale * kLog2e) || (lens && !aligned(lens, 4)))
         return TQ_ERR_INVALID_ARG;
     if (!lens && (T < 0 || T > kc->Tcap - add)) return TQ_ERR_INVALID_ARG;
     if (!attend_sizes_ok(B, Lq, Hq, kc->Hkv) || kc->Tcap >= ((int64_t)1 << 31)) return TQ_ERR_UNSUPPORTED;
@@ -249,6 +258,7 @@ tq_status tq_append_attend_int4(const tq_handle* h, int group, const void* k_new
     if (r == TQ_OK)
         r = prepare_attend(h, group, q, q_dtype, kc->B, Lq, Hq, kc, vc, pos, t0, Lq, scale, out, ws, ws_bytes, &a, &empty);
     if (r != TQ_OK || empty) return r;
+    if (caches_meet(h, group, kc, vc)) return TQ_ERR_INVALID_ARG;
     a.chained = 1;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t err = launch_int4_encode(h->d, group, kv_dtype, e, h->num_sms, s);

@@ -667,3 +667,92 @@ def test_offsets_beyond_32_bits(libtq, Lq):
     assert torch.equal(pool[100 * bb:104 * bb], pool[(n - 4) * bb:])
     assert tq.tq_device_status(h) == tq.TQ_OK
     tq.tq_destroy(h)
+
+
+@gpu
+def test_append_refuses_caches_that_share_blocks(libtq):
+    d, group, B, Hkv = 128, 64, 2, 2
+    h = tq.tq_init(d, 0)
+    bb = tq.tq_int4_block_bytes(d, group)
+    buf = torch.zeros(13 * bb, dtype=torch.uint8, device="cuda")
+    table = torch.arange(4, dtype=torch.int32, device="cuda").view(4, 1)
+    x, q = torch.randn((B, Hkv, 1, d), device="cuda"), torch.randn((B, 1, 4, d), device="cuda")
+    out = torch.zeros_like(q)
+    ws = torch.zeros(tq.tq_attend_int4_workspace_bytes(h, B, 1, 4, Hkv), dtype=torch.uint8, device="cuda")
+    flat = [tq.Int4Cache(d, group, B, Hkv, 64, buf=buf[i * bb:]) for i in (0, 3, 4)]
+    paged = [tq.Int4Cache(d, group, B, Hkv, 64, buf=buf, block_table=t, pool_blocks=13) for t in (table, table + 4)]
+
+    def step(kc, vc, scale=0.1):
+        tq.tq_append_attend_int4(h, x, x, kc, vc, q, out, ws, t0=3, scale=scale)
+
+    for kc, vc in ((flat[0], flat[0]), (flat[0], flat[1]), (flat[1], flat[0]), (paged[0], paged[0])):
+        with pytest.raises(tq.TQError):
+            step(kc, vc)
+    with pytest.raises(tq.TQError):
+        step(flat[0], flat[2], scale=3e38)             # its product with log2 e is not finite
+    torch.cuda.synchronize()
+    assert not buf.any() and not out.any()
+    step(flat[0], flat[2])
+    step(*paged)
+    assert tq.tq_device_status(h) == tq.TQ_OK and buf.any()
+    tq.tq_destroy(h)
+
+
+@gpu
+@pytest.mark.parametrize("Lq", [1, 5])
+def test_captured_serving_steps_on_pages(libtq, Lq):
+    """One graph holds a step (supply pages, append and attend, release what lies behind the tokens); it is
+    replayed over page borders and gives what a contiguous cache gives."""
+    d, group, B, Hkv, G, NB = 128, 64, 3, 2, 4, 5
+    h = tq.tq_init(d, 0)
+    pool = 2 * B * Hkv * NB
+    table = torch.full((B * Hkv, NB), -1, dtype=torch.int32, device="cuda")
+    refs = torch.zeros(pool, dtype=torch.int32, device="cuda")
+    paged = [tq.Int4Cache(d, group, B, Hkv, NB * 64, block_table=table, pool_blocks=pool) for _ in range(2)]
+    plain = [tq.Int4Cache(d, group, B, Hkv, NB * 64) for _ in range(2)]
+    pages = tq.Pages(table, refs, Hkv, paged)
+    info = torch.zeros(2, dtype=torch.int32, device="cuda")
+    pws = torch.zeros(tq.tq_pages_workspace_bytes(pages), dtype=torch.uint8, device="cuda")
+    nws = tq.tq_attend_int4_workspace_bytes(h, B, Lq, Hkv * G, Hkv)
+    ws, ws2 = (torch.zeros(nws, dtype=torch.uint8, device="cuda") for _ in range(2))
+    pos = torch.tensor([0, 50, 63], dtype=torch.int32, device="cuda")
+    zero, start = torch.zeros_like(pos), pos.clone()
+    first = torch.randn((B, Hkv, 64, d), device="cuda").bfloat16()
+    tq.tq_pages_alloc(h, pages, zero, start, info, pws)
+    for b in range(1, B):
+        for c in (paged, plain):
+            for i, x in enumerate(c):
+                rows = slice(b * Hkv, (b + 1) * Hkv)
+                one = (tq.Int4Cache(d, group, 1, Hkv, NB * 64, buf=x.buf, block_table=table[rows], pool_blocks=pool) if c is paged
+                       else tq.Int4Cache(d, group, 1, Hkv, NB * 64, buf=x.buf[b * Hkv * NB * x.block_bytes:]))
+                tq.tq_encode_int4(h, first[b:b + 1, :, :int(start[b])], one)
+    k, v = (torch.randn((B, Hkv, Lq, d), device="cuda").bfloat16() for _ in range(2))
+    q = torch.randn((B, Lq, Hkv * G, d), device="cuda").bfloat16()
+    out, ref, hi = torch.zeros_like(q), torch.zeros_like(q), torch.zeros_like(pos)
+
+    def step():
+        torch.add(pos, Lq, out=hi)
+        tq.tq_pages_alloc(h, pages, pos, hi, info, pws)
+        tq.tq_append_attend_int4(h, k, v, *paged, q, out, ws, pos=pos, scale=0.1)
+        tq.tq_pages_free(h, pages, hi)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        with torch.cuda.graph(graph, stream=side):
+            step()
+    torch.cuda.synchronize()
+    for _ in range(220 // Lq):
+        for x in (k, v, q):
+            x.copy_(torch.randn_like(x.float()).to(x.dtype))
+        graph.replay()
+        tq.tq_append_attend_int4(h, k, v, *plain, q, ref, ws2, pos=pos, scale=0.1)
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref) and int(info[1]) == 0
+        pos += Lq
+    held = (table >= 0).view(B, Hkv, NB).sum(-1)
+    assert torch.equal(held, ((pos + 63) // 64)[:, None].expand(B, Hkv).long()) and int(refs.sum()) == int(held.sum())
+    tq.tq_pages_free(h, pages, zero)
+    assert not refs.any() and tq.tq_device_status(h) == tq.TQ_OK
+    tq.tq_destroy(h)
