@@ -41,6 +41,10 @@
 //
 // Data movement: each warp owns a ring of chunks (codes and pairs of K and V,
 // four bulk copies with an mbarrier); waits are bounded as in the other kernels.
+//
+// Measured: 4 sequences of 102400 tokens, 16/8 heads, d 128, bf16 (floor 72 us): 109 us, 66 %
+// of the copy rate; the copies alone take 82 and the arithmetic alone 85 us.  64 ragged
+// sequences up to 8198 tokens, 32/8 heads, fp16 (floor 55): 120 to 125 us.
 #include <type_traits>
 
 #include "tq_frag.cuh"
@@ -630,7 +634,7 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
                 // ---- values: O^T += Cv^T (p vs).  An odd token enters as p (vz + 15 vs) - p vs (15 - c):
                 // codes are all positive and a long flat softmax would sum them to many times the
                 // result, with the tensor core's truncated additions (relative error against 64 bits
-                // at 4133 tokens 7e-5, this way below 5e-6)
+                // at 4133 tokens 7e-5; this way, and with exact picks for fp32 calls, 5e-7)
 #pragma unroll
                 for (int kt = 0; kt < NTILE; ++kt) {
                     uint32_t pb[VT][2];

@@ -19,8 +19,9 @@
 // are the two row tiles of the unit, and an expanded tile serves 256 rows; with MT = 1
 // (few rows, or fp32 at head_dim 128, whose query limbs leave no shared memory) they
 // take the even and the odd tiles and are merged at the unit's end.  Warps 8-11
-// expand the blocks, warp 13 fills their ring (bulk copies), warp 12 issues the mma (one thread), the scores of the next tiles before
-// the values of this one, so that softmax and tensor core overlap.  The mma of one
+// expand the blocks, warp 13 fills their ring (bulk copies), warp 12 issues the mma (its
+// elected lane), the scores of the next tiles before the values of this one, so that softmax
+// and tensor core overlap.  The mma of one
 // thread run in issue order, so a score buffer is not overwritten before the product
 // with the weights in it has run.  The reference exponent moves only when it is
 // exceeded by 2^8 (two limbs: 2^2); then O is rescaled, once the stream's last product is done.
@@ -28,6 +29,12 @@
 // Work: the units' tiles (each unit only as far as its last row sees) laid end
 // to end, shared out evenly over one CTA per SM on the device, cut units merged
 // by the combine kernel, as in tq_int4_attend.cu.
+//
+// Measured: 512 queries after 40448 tokens, 32/8 heads, d 128, bf16: 350 to 380 us (about
+// 0.9 PFLOP/s, 55 % of cuBLAS); a 256 x 64 tile takes about 2000 clocks, of which the tensor
+// pipe and the exponentials fill half each; the softmax warps' chain of waits, loads and
+// stores bounds it.  5 queries of 16 sequences at 4000 tokens: 50 us (20 of 128 rows used; a
+// tile's softmax again).
 //
 // NaN: a value group with a non-finite pair is expanded as zeros, and the first
 // such token of the segment is kept per group; rows that see it get NaN in that
