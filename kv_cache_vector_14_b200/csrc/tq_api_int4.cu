@@ -142,7 +142,6 @@ tq_status prepare_attend(const tq_handle* h, int group, const void* q, tq_dtype 
     a->err = h->derr;
     a->first_wait = h->first_wait >= 0 ? h->first_wait : kDefaultWaitLimit;
     a->vec16 = aligned(q, 16) && aligned(out, 16);
-    a->chained = 0;
     return device_ok(h);
 }
 
@@ -259,7 +258,6 @@ tq_status tq_append_attend_int4(const tq_handle* h, int group, const void* k_new
         r = prepare_attend(h, group, q, q_dtype, kc->B, Lq, Hq, kc, vc, pos, t0, Lq, scale, out, ws, ws_bytes, &a, &empty);
     if (r != TQ_OK || empty) return r;
     if (caches_meet(h, group, kc, vc)) return TQ_ERR_INVALID_ARG;
-    a.chained = 1;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t err = launch_int4_encode(h->d, group, kv_dtype, e, h->num_sms, s);
     if (err == cudaSuccess) err = launch_any(h, group, q_dtype, a, s);

@@ -65,7 +65,6 @@ struct Int4AttendArgs {
     int* err;
     int first_wait;
     int vec16;                // q and out start on 16-byte boundaries
-    int chained;              // launched as a programmatic dependent of the encode of its newest tokens
 };
 constexpr int kInt4MaxCtas = 256;
 // Rows of a partial slot, by which a call's kernel is known: 8 the split kernel

@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
     if (lane == 0)
         for (int s = 0; s < RING; ++s) mbar_init(smem_u32(&bar[s]), 1);
     fence_mbar_init();
-    if (a.chained) pdl_wait();                                // the newest tokens come from the encode before this
+    pdl_wait();                                               // (the newest tokens come from the encode before this)
 
     // ---------------- this CTA's share [lo, hi) of the chunks
     const int rgroups = (a.rows + ROWS - 1) / ROWS;
@@ -781,12 +781,7 @@ cudaError_t launch_t(const Int4AttendArgs& a, int num_sms, cudaStream_t s) {
     cudaError_t e = set_smem_once<tq_int4_attend_kernel<D, GRP, NT, DT>>(S::kSmem);
     if (e != cudaSuccess) return e;
     const int ctas = num_sms < kInt4MaxCtas ? num_sms : kInt4MaxCtas;
-    if (a.chained) {
-        e = launch_pdl(tq_int4_attend_kernel<D, GRP, NT, DT>, dim3(ctas), dim3(S::kNW * 32), S::kSmem, s, a);
-    } else {
-        tq_int4_attend_kernel<D, GRP, NT, DT><<<ctas, S::kNW * 32, S::kSmem, s>>>(a);
-        e = cudaGetLastError();
-    }
+    e = launch_pdl(tq_int4_attend_kernel<D, GRP, NT, DT>, dim3(ctas), dim3(S::kNW * 32), S::kSmem, s, a);
     if (e != cudaSuccess) return e;
     return launch_int4_combine<D, DT>(a, S::kRows, ctas, s);
 }

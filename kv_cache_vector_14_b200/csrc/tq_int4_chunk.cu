@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
         tc_alloc(smem_u32(tmem_slot), 512);
         tc_relinquish();
     }
-    if (a.chained) pdl_wait();
+    pdl_wait();
 
     // ---------------- this CTA's share of the tiles: pairs (sequence, row tile) in order, each
     // Hkv units of unit_tiles tiles; a scan over runs of pairs finds the place
@@ -842,12 +842,7 @@ cudaError_t launch_t(const Int4AttendArgs& a, int num_sms, cudaStream_t s) {
     cudaError_t e = set_smem_once<tq_int4_chunk_kernel<D, GRP, DT, MT>>(C::kSmem);
     if (e != cudaSuccess) return e;
     const int ctas = num_sms < kInt4MaxCtas ? num_sms : kInt4MaxCtas;
-    if (a.chained) {
-        e = launch_pdl(tq_int4_chunk_kernel<D, GRP, DT, MT>, dim3(ctas), dim3(kThreads), C::kSmem, s, a);
-    } else {
-        tq_int4_chunk_kernel<D, GRP, DT, MT><<<ctas, kThreads, C::kSmem, s>>>(a);
-        e = cudaGetLastError();
-    }
+    e = launch_pdl(tq_int4_chunk_kernel<D, GRP, DT, MT>, dim3(ctas), dim3(kThreads), C::kSmem, s, a);
     if (e != cudaSuccess) return e;
     return launch_int4_combine_tiles<D, DT, MT>(a, ctas, s);
 }

@@ -17,6 +17,7 @@ __global__ void __launch_bounds__(32 * kCombineWarps) tq_int4_combine_kernel(con
                                                                             int slot_rows) {
     constexpr int E = D / 32;
     const int c = blockIdx.x, r = blockIdx.y * kCombineWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    pdl_trigger();
     pdl_wait();
     const int4 s = a.split[c];
     if (!s.w) return;
@@ -86,6 +87,7 @@ __global__ void __launch_bounds__(128) tq_int4_combine_tiles_kernel(const __grid
     constexpr int R = 128 * MT;
     const int c = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * 32 + lane;
     const int col = blockIdx.z * 32 + (threadIdx.x >> 5) * 8;
+    pdl_trigger();
     pdl_wait();
     const int4 s = a.split[c];
     if (!s.w) return;

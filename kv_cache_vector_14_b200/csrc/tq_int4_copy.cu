@@ -199,7 +199,8 @@ template <int D, int GRP, int DT>
 __global__ void __launch_bounds__(kThreads) tq_int4_encode_kernel(const Int4CopyArgs a, uint32_t nitems) {
     constexpr int kW = D / kVals;             // threads per vector
     constexpr int kL = GRP / kVals;           // lanes per group
-    pdl_trigger();                            // an attention chained to this encode may start its set-up
+    pdl_trigger();                            // the kernel behind this one may start its set-up
+    pdl_wait();
     const Int4Side& sd = a.side[blockIdx.y];
     const uint32_t stride = gridDim.x * kThreads;
     // (a warp goes out of range as a whole vector at a time: nitems is a multiple of kW, and the
@@ -271,6 +272,8 @@ template <int D, int GRP, int DT>
 __global__ void __launch_bounds__(kThreads) tq_int4_expand_kernel(const Int4CopyArgs a, uint32_t nitems) {
     using E = Elem<DT>;
     constexpr int kW = D / kVals, kL = GRP / kVals;
+    pdl_trigger();
+    pdl_wait();
     const Int4Side& sd = a.side[blockIdx.y];
     const uint32_t stride = gridDim.x * kThreads;
     for (uint32_t i0 = blockIdx.x * kThreads + threadIdx.x; i0 < nitems; i0 += kUnroll * stride) {
@@ -328,11 +331,8 @@ cudaError_t launch_copy(bool encode, const Int4CopyArgs& a, int num_sms, cudaStr
     const uint32_t need = (nitems + kThreads - 1) / kThreads;
     const uint32_t most = (uint32_t)num_sms * 8;
     const dim3 grid(need < most ? need : most, (unsigned)a.nsides);
-    if (encode)
-        tq_int4_encode_kernel<D, GRP, DT><<<grid, kThreads, 0, s>>>(a, nitems);
-    else
-        tq_int4_expand_kernel<D, GRP, DT><<<grid, kThreads, 0, s>>>(a, nitems);
-    return cudaGetLastError();
+    return launch_pdl(encode ? tq_int4_encode_kernel<D, GRP, DT> : tq_int4_expand_kernel<D, GRP, DT>, grid, dim3(kThreads), 0, s,
+                      a, nitems);
 }
 
 template <int D, int GRP>

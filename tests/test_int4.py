@@ -756,3 +756,73 @@ def test_captured_serving_steps_on_pages(libtq, Lq):
     tq.tq_pages_free(h, pages, zero)
     assert not refs.any() and tq.tq_device_status(h) == tq.TQ_OK
     tq.tq_destroy(h)
+
+
+@gpu
+@pytest.mark.parametrize("Lq", [1, 20])
+def test_calls_behind_joined_streams(libtq, Lq):
+    """Every call waits for what its stream waits for, eagerly and captured: inputs made by slow kernels on two
+    other streams, outputs read by a third."""
+    d, group, B, Hkv, G = 128, 64, 2, 2, 4
+    cs, _, _ = _filled(d, group, B, Hkv, 320, 9)
+    h, (kc, vc) = cs.h, cs.caches
+    pos = torch.tensor([100, 250], dtype=torch.int32, device="cuda")
+    ws = torch.zeros(tq.tq_attend_int4_workspace_bytes(h, B, Lq, Hkv * G, Hkv), dtype=torch.uint8, device="cuda")
+    seed_kv = torch.randn((B, Hkv, Lq, d), device="cuda").bfloat16()
+    seed_q = torch.randn((B, Lq, Hkv * G, d), device="cuda").bfloat16()
+    kv, q, out = torch.zeros_like(seed_kv), torch.zeros_like(seed_q), torch.zeros_like(seed_q)
+    back, read = torch.zeros_like(seed_kv), [torch.zeros_like(seed_q), torch.zeros_like(seed_kv)]
+    slow = torch.randn((4096, 4096), device="cuda")
+    table = torch.full((B * Hkv, 5), -1, dtype=torch.int32, device="cuda")
+    refs = torch.zeros(40, dtype=torch.int32, device="cuda")
+    pages = tq.Pages(table, refs, Hkv, [])
+    pws = torch.zeros(tq.tq_pages_workspace_bytes(pages), dtype=torch.uint8, device="cuda")
+    lo, hi, seen = torch.zeros_like(pos), torch.zeros_like(pos), torch.zeros_like(table)
+    s1, s2, s3 = (torch.cuda.Stream() for _ in range(3))
+
+    def run(main):
+        for s in (s1, s2, s3):
+            s.wait_stream(main)
+        with torch.cuda.stream(s1):
+            (slow @ slow)
+            kv.copy_(seed_kv)
+            hi.copy_(pos)
+        with torch.cuda.stream(s2):
+            (slow @ slow) @ slow
+            q.copy_(seed_q)
+        main.wait_stream(s1)
+        main.wait_stream(s2)
+        tq.tq_append_attend_int4(h, kv, kv, kc, vc, q, out, ws, pos=pos, scale=0.1)
+        tq.tq_expand_int4(h, kc, back, pos=pos)
+        tq.tq_pages_alloc(h, pages, lo, hi, None, pws)
+        s3.wait_stream(main)
+        with torch.cuda.stream(s3):
+            read[0].copy_(out)
+            read[1].copy_(back)
+            seen.copy_(table)
+        main.wait_stream(s3)
+        tq.tq_pages_free(h, pages, lo)
+
+    def check():
+        torch.cuda.synchronize()
+        want, wb = torch.zeros_like(out), torch.zeros_like(back)
+        tq.tq_attend_int4(h, seed_q, kc, vc, want, ws, seq_lens=pos + Lq, scale=0.1)
+        tq.tq_expand_int4(h, kc, wb, pos=pos)
+        assert torch.equal(read[0], want) and torch.equal(read[1], wb) and want.abs().sum() > 0
+        assert torch.equal((seen >= 0).sum(1).view(B, Hkv), ((pos + 63) // 64)[:, None].expand(B, Hkv).long())
+        assert (table == -1).all() and not refs.any()
+        for t in (kv, q, out, back, hi, seen, *read):
+            t.zero_()
+        torch.cuda.synchronize()
+
+    run(torch.cuda.current_stream())
+    check()
+    main = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(main):
+        with torch.cuda.graph(graph, stream=main):
+            run(main)
+    for _ in range(2):
+        graph.replay()
+        check()
+    cs.close()
