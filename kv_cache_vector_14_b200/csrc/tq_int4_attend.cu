@@ -42,9 +42,9 @@
 // Data movement: each warp owns a ring of chunks (codes and pairs of K and V,
 // four bulk copies with an mbarrier); waits are bounded as in the other kernels.
 //
-// Measured: 4 sequences of 102400 tokens, 16/8 heads, d 128, bf16 (floor 72 us): 109 us, 66 %
+// Measured: 4 sequences of 102400 tokens, 16/8 heads, d 128, bf16 (floor 72 us): 108 us, 67 %
 // of the copy rate; the copies alone take 82 and the arithmetic alone 85 us.  64 ragged
-// sequences up to 8198 tokens, 32/8 heads, fp16 (floor 55): 120 to 125 us.
+// sequences up to 8198 tokens, 32/8 heads, fp16 (floor 55): 119 to 123 us.
 #include <type_traits>
 
 #include "tq_frag.cuh"

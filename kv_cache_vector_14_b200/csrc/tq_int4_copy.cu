@@ -13,8 +13,8 @@
 // addition of 1.5 2^18 (where an fp32 ulp is 1/32), the clamp to 15 one packed
 // minimum per two values, and 16-bit inputs take their minimum and maximum two
 // values at a time.  Measured on 262144 vectors of 128 bf16 values (floor 13 us):
-// encode 54 us with 8 values per thread and separate steps, 24 us this way (issue slots
-// 72 % used, ALU 62 %), expand 24 us.
+// encode 54 us with 8 values per thread and separate steps, 23 us this way (issue slots
+// 72 % used, ALU 62 %), expand 23 us.
 #include "tq_int4.h"
 
 namespace tqi {
