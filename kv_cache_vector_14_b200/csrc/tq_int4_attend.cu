@@ -24,7 +24,7 @@
 //     alone (2^-11 relative, against 2^-8 of the output's rounding).
 // The products with the zeros are rank-one: fp32 sums outside the tensor core.
 // To keep p vs inside fp16 whatever the values' magnitude, the reference
-// exponent m follows the maximum of s_t + log2 max_G vs_{t,G} rather than of s_t.
+// exponent m follows the maximum of s_t + log2 max_G |vs_{t,G}| rather than of s_t.
 //   scores  S[16 tok][8] += C[16 tok][32] Q[32][8]                   (int8, group/32 steps per group)
 //   values  O^T[16 values][8] += Cv^T[16 values][16 tok] P[16 tok][8], one P per group
 // Lane (g, t) = (lane / 4, lane % 4) owns tokens g and g + 8 of a 16-token tile
@@ -574,7 +574,8 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
                         }
                     }
                 }
-                // ---- the values' scales and zeros, and a bound of log2 of the scales
+                // ---- the values' scales and zeros, and a bound of log2 of the scales' magnitudes (where a
+                // group's zero rounds above its maximum the scale is below zero)
                 const uint8_t* vp = st + S::kOffVp + (k0 * 16 + gr) * S::kPairB;
                 uint32_t vpair[NP][NG];
                 float lg[NP];
@@ -584,7 +585,7 @@ __global__ void __launch_bounds__(Shape<D, GRP, NT>::kNW * 32, 1) tq_int4_attend
 #pragma unroll
                     for (int gam = 0; gam < NG; ++gam) {
                         vpair[k][gam] = *reinterpret_cast<const uint32_t*>(vp + 8 * k * S::kPairB + 4 * gam);
-                        big = fmaxf(big, __low2float(*reinterpret_cast<const __half2*>(&vpair[k][gam])));
+                        big = fmaxf(big, fabsf(__low2float(*reinterpret_cast<const __half2*>(&vpair[k][gam]))));
                     }
                     lg[k] = fast_log2(big);
                 }

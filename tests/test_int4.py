@@ -826,3 +826,55 @@ def test_calls_behind_joined_streams(libtq, Lq):
         graph.replay()
         check()
     cs.close()
+
+
+def check_attend(d, group, dtype, kx, vx, qx, T, scale, limit=False):
+    """Attention of qx [B, Lq, Hq, d] over T tokens of kx, vx [B, Hkv, T, d] encoded from fp32, every row against the
+    oracle.  limit: values at the fp16 limit, whose bf16 operands stop at 65504: the top of a group lies at most
+    15 scale 2^-11 <= 2^-10 V above it (scale rounded to 2^-11), so 2^-10 V on values and 2^-10 S on scores more."""
+    B, Hkv = kx.shape[:2]
+    Lq, G = qx.shape[1], qx.shape[2] // Hkv
+    cs = Case(d, group, B, Hkv, -(-T // 64) * 64)
+    for c, x in zip(cs.caches, (kx, vx)):
+        tq.tq_encode_int4(cs.h, to_gpu(x, "f32"), c)
+    q = to_gpu(qx, dtype)
+    ws = torch.zeros(tq.tq_attend_int4_workspace_bytes(cs.h, B, Lq, Hkv * G, Hkv), dtype=torch.uint8, device="cuda")
+    out = torch.full_like(q, float("nan"))
+    tq.tq_attend_int4(cs.h, q, *cs.caches, out, ws, T=T, scale=scale)
+    half = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[dtype]
+    got, qn = as_np(out).astype(np.float64), as_np(q).astype(np.float64)
+    rounded = dtype == "bf16" and Lq * G > 8
+    for b in range(B):
+        for hh in range(Hkv):
+            kc, ks, kz = U.quantise(kx[b, hh], group)
+            k, v = U.values(kc, ks, kz, group), U.grid(vx[b, hh], group)
+            kabs = U.values(kc, np.abs(ks), np.abs(kz), group)
+            for g in range(G):
+                rows = qn[b, :, hh * G + g]
+                ref = U.attend(rows, k, v, scale, Lq)
+                bound = U.attend_bound(rows, kabs, v, scale, ref, half, bf16=dtype == "bf16", rounded=rounded)
+                if limit and rounded:
+                    S = abs(scale) * (np.abs(rows) @ kabs.T).max(-1, keepdims=True)
+                    bound = bound + np.abs(v).max() * 2.0 ** -10 * (1 + 2 * S)
+                if dtype == "f16":
+                    bound = bound + 2.0 ** -25
+                err = np.abs(got[b, :, hh * G + g] - ref)
+                assert np.isfinite(got[b, :, hh * G + g]).all() and (err <= bound).all(), (b, hh, g, err.max(), bound.max())
+    cs.close()
+
+
+@gpu
+@pytest.mark.parametrize("d,group", [(64, 32), (128, 64), (128, 128), (256, 64)])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("Lq,T", [(1, 1), (1, 40), (2, 333), (12, 333)])
+def test_constant_value_groups(libtq, d, group, dtype, Lq, T):
+    """fp32 groups of one value: where the zero rounds above it the scale is negative (and no code uses it).  All
+    tokens like that, and half of them beside ordinary ones."""
+    rng = np.random.default_rng(d + T)
+    for const in (0.3, 0.7, -0.1, 40020.0):
+        vx = np.full((2, 1, T, d), const, np.float32)
+        vx[1, 0, ::2] = rng.standard_normal((len(vx[1, 0, ::2]), d)) * min(abs(const), 1000.0)
+        scales = U.quantise(vx[0, 0], group)[1]
+        assert const == 40020.0 or (scales < 0).all() == (np.float32(np.float16(const)) > np.float32(const))
+        check_attend(d, group, dtype, rand(rng, (2, 1, T, d)), vx, rng.standard_normal((2, Lq, 2, d)).astype(np.float32),
+                     T, d ** -0.5)
