@@ -549,7 +549,8 @@ tq_status tq_append_attend(const tq_handle* h, const void* k_new, const void* v_
     cudaError_t e = cudaSuccess;
     const bool chained = !empty_k;
     if (chained) {
-        // K encode as a plain launch, V encode and the prologue as its
+        // K encode as a plain launch (or, in bulk, one that lets the next start only once
+        // everything before this call is complete), V encode and the prologue as its
         // programmatic dependents (each completes only after its predecessor);
         // the split-K kernel sets up while they run and reads the cache and
         // the query operands after it waits.

@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kRThreads, 1)
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kOffBar);
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::kOffMisc);
-    pdl_trigger();                 // a chained kernel may start (it waits for this one's writes)
+    if (!a.wait_x) pdl_trigger();  // a chained kernel may start (it waits for this one's writes)
 
     const int tid = threadIdx.x, warp = tid >> 5;
     const int64_t N = a.B * a.Hkv * a.Tnew;
@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(kRThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (a.wait_x) pdl_trigger();   // the copy thread has waited: all before this kernel is complete (see launch_pdl)
 
     if (tid == kRQuant) {
         // ======================================== copy and mma thread
@@ -487,7 +488,7 @@ __global__ void __launch_bounds__(k6Threads, 2)
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kOffBar);
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::kOffMisc);
-    pdl_trigger();                 // a chained kernel may start (it waits for this one's writes)
+    if (!a.wait_x) pdl_trigger();  // a chained kernel may start (it waits for this one's writes)
 
     const int tid = threadIdx.x, warp = tid >> 5;
     const int64_t N = a.B * a.Hkv * a.Tnew;
@@ -547,6 +548,7 @@ __global__ void __launch_bounds__(k6Threads, 2)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (a.wait_x) pdl_trigger();   // the copy thread has waited: all before this kernel is complete (see launch_pdl)
 
     if (tid == k6Quant) {
         // ======================================== copy and mma thread
@@ -802,7 +804,7 @@ __global__ void __launch_bounds__(kVThreads, 2)
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kOffBar);
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + S::kOffMisc);
-    pdl_trigger();                 // a chained kernel may start (it waits for this one's writes)
+    if (!a.wait_x) pdl_trigger();  // a chained kernel may start (it waits for this one's writes)
 
     const int tid = threadIdx.x, warp = tid >> 5;
     const int64_t N = a.B * a.Hkv * a.Tnew;
@@ -858,6 +860,7 @@ __global__ void __launch_bounds__(kVThreads, 2)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (a.wait_x) pdl_trigger();   // the copy thread has waited: all before this kernel is complete (see launch_pdl)
 
     if (tid == kVQuant) {
         // ======================================== copy and mma thread
@@ -1061,7 +1064,9 @@ bool rot_tensor_map(int d, tq_dtype dt, const EncArgs& a, CUtensorMap* tm) {
 // set-up (barriers, tensor memory, the rotation operand, the JL operand copy) overlaps that
 // kernel's end.  A chained launch (pdl: the previous kernel writes neither this input nor the
 // cache range) loads at once; any other waits for the previous kernel before its first input
-// load, and every write of the kernel follows that load.
+// load, and every write of the kernel follows that load.  It lets its own dependents start only
+// after that wait: a chained one reads inputs and block tables at once, which the kernel in
+// front of this one may still be writing.
 EncArgs dependent_args(const EncArgs& a, bool chained) {
     EncArgs b = a;
     b.wait_x = chained ? 0 : 1;

@@ -206,6 +206,16 @@ __device__ __forceinline__ void encode_locate(const EncArgs& a, uint32_t gv, int
 // while the previous kernel on the stream is still running; it must execute
 // pdl_wait() before reading anything that kernel writes.  pdl_trigger() lets
 // the next kernel start launching.
+//
+// Who may do what.  A kernel that triggers before its own pdl_wait() lets the
+// next one start while the kernel before itself still runs.  So:
+//   * every kernel launched with launch_pdl waits before it completes (the wait
+//     of the next one then covers all kernels before it, too);
+//   * a kernel that reads inputs, tables or caches without waiting, because the
+//     kernels chained in front of it by its own call do not write them, stands
+//     behind a first kernel of that call that triggers only once everything
+//     before the call is complete: a plain launch, or a trigger after the wait;
+//   * every other kernel waits before its first read of what a caller gave it.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

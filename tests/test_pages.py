@@ -395,3 +395,65 @@ def test_beam_serving_run(libtq, kind):
     assert not refs.any() and (table == -1).all()
     assert tq.tq_device_status(h) == tq.TQ_OK
     tq.tq_destroy(h)
+
+
+@gpu
+@pytest.mark.parametrize("d,dtype", [(128, torch.bfloat16), (64, torch.float16)])
+@pytest.mark.parametrize("before", ["fork", "alloc", "compact", "expand"])
+def test_bulk_append_behind_a_call_that_writes_what_it_reads(libtq, d, dtype, before):
+    """A bulk tq_append_attend (whose encodes and attention are chained) directly behind a call that writes the block
+    table or the new values gives what it gives after a synchronisation.  A slow product first, so that the launches
+    stand ready behind each other."""
+    B, Hkv, G, T0, Tnew, NB = 16, 2, 2, 1024, 512, 64
+    pool, h = 2 * B * Hkv * NB, tq.tq_init(d, 0)
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    lens = T0 if before == "alloc" else T0 + Tnew
+    table0 = torch.full((B * Hkv, NB), -1, dtype=torch.int32, device="cuda")
+    place = torch.randperm(pool, generator=gen, device="cuda").to(torch.int32)
+    table0[:, :lens // 64] = place[:B * Hkv * (lens // 64)].view(B * Hkv, -1)
+    refs0 = torch.zeros(pool, dtype=torch.int32, device="cuda")
+    refs0[table0[table0 >= 0].long()] = 1
+    table, refs = table0.clone(), refs0.clone()
+    caches = [tq.Cache(d, k, B, Hkv, NB * 64, block_table=table, pool_blocks=pool) for k in (True, False)]
+    pages = tq.Pages(table, refs, Hkv, caches)
+    pws = torch.zeros(tq.tq_pages_workspace_bytes(pages), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(tq.tq_attend_workspace_bytes(h, B, Hkv * G, Hkv, NB * 64), dtype=torch.uint8, device="cuda")
+    k, v = (torch.randn((B, Hkv, Tnew, d), generator=gen, device="cuda").to(dtype) for _ in range(2))
+    prefix = [torch.randn((B, Hkv, T0, d), generator=gen, device="cuda").to(dtype) for _ in range(2)]
+    q = torch.randn((B, Hkv * G, d), generator=gen, device="cuda").to(dtype)
+    four = tq.Int4Cache(d, 32, B, Hkv, Tnew)
+    tq.tq_encode_int4(h, torch.randn((B, Hkv, Tnew, d), generator=gen, device="cuda"), four)
+    swap = i32(np.arange(B) ^ 1)
+    lo, hi = i32([T0] * B), i32([T0 + Tnew] * B)
+    slow = torch.randn((4096, 4096), device="cuda")
+
+    def run(apart):
+        table.copy_(table0)
+        refs.copy_(refs0)
+        v.zero_() if before == "expand" else None
+        for c in caches:
+            c.buf.zero_()
+        tq.tq_encode_k(h, prefix[0], caches[0], 0)
+        tq.tq_encode_v(h, prefix[1], caches[1], 0)
+        out = torch.zeros((B, Hkv * G, d), device="cuda")
+        torch.cuda.synchronize()
+        slow @ slow
+        if before == "fork":
+            tq.tq_pages_fork(h, pages, swap)
+        elif before == "alloc":
+            tq.tq_pages_alloc(h, pages, lo, hi, None, pws)
+        elif before == "compact":
+            tq.tq_pages_compact(h, pages, None, pws)
+        else:
+            tq.tq_expand_int4(h, four, v)
+        if apart:
+            torch.cuda.synchronize()
+        tq.tq_append_attend(h, k, v, *caches, T0, q, out, ws, scale=0.09)
+        assert tq.tq_device_status(h) == tq.TQ_OK
+        return [out, *(c.buf.clone() for c in caches), table.clone()]
+
+    want = run(True)
+    for _ in range(3):
+        for a, b in zip(run(False), want):
+            assert torch.equal(a, b)
+    tq.tq_destroy(h)
