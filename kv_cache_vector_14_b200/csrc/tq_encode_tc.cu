@@ -345,7 +345,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) tq_encode_k128_tc_kernel(const
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBar);     // [0] JL image copy, [1..2] mma done
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kOffBar + 32);
     uint8_t* scode = sm + kOffCode;
-    pdl_trigger();                 // a chained kernel may start (it waits for this one's writes)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 3, l = lane & 7;
     const int64_t N = a.B * a.Hkv * a.Tnew;
@@ -367,6 +366,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) tq_encode_k128_tc_kernel(const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    pdl_trigger();                 // a chained kernel may start (it waits for this one's writes)
     if (threadIdx.x == 0) {
         mbar_expect_tx(bar_b, 2 * kOpBytes);
         bulk_g2s(sbase + kOffBhi, a.bimg, 2 * kOpBytes, bar_b);

@@ -215,7 +215,11 @@ __device__ __forceinline__ void encode_locate(const EncArgs& a, uint32_t gv, int
 //     kernels chained in front of it by its own call do not write them, stands
 //     behind a first kernel of that call that triggers only once everything
 //     before the call is complete: a plain launch, or a trigger after the wait;
-//   * every other kernel waits before its first read of what a caller gave it.
+//   * every other kernel waits before its first read of what a caller gave it;
+//   * a kernel with tensor memory allocates it before it triggers (the chained V
+//     encode alone does not: the rest of its call holds none until it is done).  A
+//     dependent that took an SM's columns first and then waited for a kernel that
+//     still has to allocate there would wait for good.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

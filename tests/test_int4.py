@@ -878,3 +878,34 @@ def test_constant_value_groups(libtq, d, group, dtype, Lq, T):
         assert const == 40020.0 or (scales < 0).all() == (np.float32(np.float16(const)) > np.float32(const))
         check_attend(d, group, dtype, rand(rng, (2, 1, T, d)), vx, rng.standard_normal((2, Lq, 2, d)).astype(np.float32),
                      T, d ** -0.5)
+
+
+@gpu
+@pytest.mark.parametrize("d,dtype", [(64, "bf16"), (128, "bf16"), (128, "f16")])
+@pytest.mark.parametrize("Tnew", [40, 1024])
+def test_chunks_between_turboquant_encodes(libtq, d, dtype, Tnew):
+    """Tensor-core encodes of a TurboQuant cache (small and bulk) and 4-bit chunks back to back on one stream: both
+    hold tensor memory, and each starts its set-up while the one before it runs."""
+    B, Hkv, G, Lq, T = 8, 2, 4, 20, 320
+    cs, _, rng = _filled(d, 32, B, Hkv, T, 2)
+    x = to_gpu(rng.standard_normal((B, Hkv, Tnew, d)).astype(np.float32), "bf16")
+    q = to_gpu(rng.standard_normal((B, Lq, Hkv * G, d)).astype(np.float32), dtype)
+    caches = [tq.Cache(d, k, B, Hkv, 1024) for k in (True, False)]
+    ws = torch.zeros(tq.tq_attend_int4_workspace_bytes(cs.h, B, Lq, Hkv * G, Hkv), dtype=torch.uint8, device="cuda")
+
+    def run(outs, apart):
+        for out in outs:
+            for f, c in zip((tq.tq_encode_k, tq.tq_encode_v), caches):
+                f(cs.h, x, c, 0)
+                tq.tq_attend_int4(cs.h, q, *cs.caches, out, ws, T=T, scale=0.1)
+                if apart:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return outs, [c.buf.clone() for c in caches]
+
+    want, stored = run([torch.zeros_like(q)], True)
+    for c in caches:
+        c.buf.zero_()
+    got, again = run([torch.zeros_like(q) for _ in range(20)], False)
+    assert all(torch.equal(o, want[0]) for o in got) and all(torch.equal(a, b) for a, b in zip(stored, again))
+    cs.close()
