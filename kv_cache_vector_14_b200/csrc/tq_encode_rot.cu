@@ -437,6 +437,9 @@ __global__ void __launch_bounds__(kRThreads, 1)
             }
         }
         if constexpr (IS_K) {
+            // the last tile's sgn_at, written by thread c = 0 of each vector behind a look-up of
+            // the block table; within the loop the next tile's exchange lies between
+            named_bar_r(1 + (warp & 3), 4 * 32);
             if (!failed && n > 0 && !signs(n - 1)) failed = true;
         }
         if (failed && (tid & 31) == 0) atomicExch(a.err, 1);

@@ -870,3 +870,30 @@ def test_attend_argument_errors(handles):
     with pytest.raises(ValueError):                                # a K cache is not a PolarQuant-only K cache
         tq.tq_attend_decode_polar(h, q, kc, vc, out, ws, T=10)
     assert tq.tq_device_status(h) == tq.TQ_OK
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("T", [512, 1100])
+def test_bulk_k_encode_into_paged_cache_with_cold_table(handles, d, T):
+    """Bulk K encodes (one tile and several per CTA) into a paged cache whose block table comes from memory: the
+    look-up takes longest then, and the sign words of every tile still go to the record that it names."""
+    B, Hkv, NB = 16, 2, 20
+    h = handles[d]
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn((B, Hkv, T, d), generator=gen, device="cuda").bfloat16()
+    plain = tq.Cache(d, True, B, Hkv, NB * 64)
+    tq.tq_encode_k(h, x, plain, 0)
+    bb, pool = tq.tq_block_bytes(d, True), 2 * B * Hkv * NB
+    sweep = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")           # larger than L2
+    for _ in range(10):
+        table = torch.randperm(pool, generator=gen, device="cuda")[:B * Hkv * NB].to(torch.int32).view(B * Hkv, NB)
+        paged = tq.Cache(d, True, B, Hkv, NB * 64, block_table=table, pool_blocks=pool)
+        sweep.zero_()
+        tq.tq_encode_k(h, x, paged, 0)
+        got = paged.buf[:pool * bb].view(pool, bb)[table.view(-1).long()]
+        assert torch.equal(got.view(-1), plain.buf[:B * Hkv * NB * bb])
+        used = torch.zeros(pool, dtype=torch.bool, device="cuda")
+        used[table.view(-1).long()] = True
+        assert not paged.buf[:pool * bb].view(pool, bb)[~used].any()
+    assert tq.tq_device_status(h) == tq.TQ_OK
