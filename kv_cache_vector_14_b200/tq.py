@@ -377,9 +377,30 @@ class Int4Cache:
         self.block_bytes, self.nbytes = bb, nbytes
         self.block_table, self.pool_blocks = block_table, pool_blocks
         self.buf = buf if buf is not None else torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=device)
+        self._dev = _one_device("Int4Cache", self.buf, block_table)
         table = C.c_void_p(block_table.data_ptr()) if block_table is not None else None
         self.struct = tq_cache(C.c_void_p(self.buf.data_ptr()), B, Hkv, Tcap, table, pool_blocks)
         self._ref = C.byref(self.struct)
+
+
+def _one_device(name: str, *tensors) -> int:
+    """Device index (-1: not CUDA) that the tensors of one object share; None: no tensor."""
+    at = {t.get_device() for t in tensors if t is not None}
+    if len(at) != 1:
+        raise ValueError(f"{name}: the tensors must lie on one device")
+    return at.pop()
+
+
+def _here(name: str, dev: int, *tensors) -> None:
+    """Refuse a call whose caches or pages (on device dev) and tensors (None: no tensor) do not all lie on the
+    current CUDA device: its kernels follow their pointers."""
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name}: all tensors must lie on the current CUDA device")
+    if _device is None:
+        _torch_accessors()
+    if dev < 0 or dev != _device():
+        raise ValueError(f"{name}: all tensors must lie on the current CUDA device")
 
 
 def _int32(t, name: str, n: int):
@@ -403,6 +424,7 @@ def _int4_copy(fn, name, h, x, cache: Int4Cache, t0: int, pos, stream):
     shape, strides = x.shape, x.stride()
     if len(shape) != 4 or shape[3] != d or strides[3] != 1:
         raise ValueError(f"{name}: the vectors must be [B, Hkv, T, {d}] with a contiguous last dim")
+    _here(name, cache._dev, x, pos)
     B, Hkv, T, _ = shape
     sb, sh, st_, _ = strides
     _check(fn(h, cache.group, x.data_ptr(), _dtype_code(x), B, Hkv, T, sb, sh, st_, cache._ref,
@@ -438,6 +460,7 @@ def tq_attend_int4(h, q, kc: Int4Cache, vc: Int4Cache, out, ws, T: int = 0, seq_
     sequence of seq_lens[b] (or T) tokens; out has q's shape and dtype."""
     d = _same_group("tq_attend_int4", h, kc, vc)
     B, Lq, Hq = _int4_queries("tq_attend_int4", d, q, out)
+    _here("tq_attend_int4", kc._dev, vc.buf, q, out, ws, seq_lens)
     _check(lib().tq_attend_int4(h, kc.group, q.data_ptr(), _dtype_code(q), B, Lq, Hq, kc._ref, vc._ref,
                                 _int32(seq_lens, "seq_lens", B), T, scale, out.data_ptr(), ws.data_ptr(),
                                 ws.numel() * ws.element_size(), _stream(stream)), "tq_attend_int4")
@@ -453,6 +476,7 @@ def tq_append_attend_int4(h, k_new, v_new, kc: Int4Cache, vc: Int4Cache, q, out,
             k_new.dtype != v_new.dtype or k_new.stride(3) != 1 or tuple(k_new.shape) != (B, kc.Hkv, Lq, d):
         raise ValueError(f"tq_append_attend_int4: k_new, v_new must be [{B}, {kc.Hkv}, {Lq}, {d}] with equal dtype "
                          "and strides and a contiguous last dim")
+    _here("tq_append_attend_int4", kc._dev, vc.buf, k_new, v_new, q, out, ws, pos)
     sb, sh, st_, _ = k_new.stride()
     _check(lib().tq_append_attend_int4(h, kc.group, k_new.data_ptr(), v_new.data_ptr(), _dtype_code(k_new), Lq, sb, sh,
                                        st_, kc._ref, vc._ref, _int32(pos, "pos", B), t0, q.data_ptr(), _dtype_code(q),
@@ -488,6 +512,7 @@ class Pages:
             raise ValueError("at most 128 buffers")
         self.block_table, self.refs, self.Hkv, self.buffers = block_table, refs, Hkv, pairs
         self.B, self.pool_blocks = block_table.shape[0] // Hkv, refs.numel()
+        self._dev = _one_device("Pages", block_table, refs, *[t for t, _ in pairs])
         self._bases = (C.c_void_p * max(1, len(pairs)))(*[t.data_ptr() for t, _ in pairs])
         self._bytes = (C.c_int64 * max(1, len(pairs)))(*[n for _, n in pairs])
         self.struct = tq_pages(block_table.data_ptr(), refs.data_ptr(), self.B, Hkv, block_table.shape[1],
@@ -502,6 +527,7 @@ def tq_pages_workspace_bytes(pages: Pages) -> int:
 def tq_pages_alloc(h, pages: Pages, lo, hi, info, ws, stream=None) -> None:
     """Make tokens [lo[b], hi[b]) writable: missing pages are supplied, shared ones
     copied.  info (int32 [2] or None): free pages left, blocks left without."""
+    _here("tq_pages_alloc", pages._dev, lo, hi, info, ws)
     _check(lib().tq_pages_alloc(h, pages._ref, _int32(lo, "lo", pages.B), _int32(hi, "hi", pages.B),
                                 _int32(info, "info", 2), ws.data_ptr(), ws.nbytes,
                                 _stream(stream)), "tq_pages_alloc")
@@ -509,22 +535,26 @@ def tq_pages_alloc(h, pages: Pages, lo, hi, info, ws, stream=None) -> None:
 
 def tq_pages_fork(h, pages: Pages, parent, stream=None) -> None:
     """Every sequence b takes the pages of parent[b] (b: unchanged, -1: none)."""
+    _here("tq_pages_fork", pages._dev, parent)
     _check(lib().tq_pages_fork(h, pages._ref, _int32(parent, "parent", pages.B), _stream(stream)), "tq_pages_fork")
 
 
 def tq_pages_free(h, pages: Pages, keep, stream=None) -> None:
     """Release the blocks behind the first keep[b] tokens of every sequence."""
+    _here("tq_pages_free", pages._dev, keep)
     _check(lib().tq_pages_free(h, pages._ref, _int32(keep, "keep", pages.B), _stream(stream)), "tq_pages_free")
 
 
 def tq_pages_compact(h, pages: Pages, info, ws, stream=None) -> None:
     """Move the live pages into the lowest places.  info: free pages, pages moved."""
+    _here("tq_pages_compact", pages._dev, info, ws)
     _check(lib().tq_pages_compact(h, pages._ref, _int32(info, "info", 2), ws.data_ptr(),
                                   ws.numel() * ws.element_size(), _stream(stream)), "tq_pages_compact")
 
 
 def tq_pages_copy(h, src_pages: Pages, dst_pages: Pages, src, dst, stream=None) -> None:
     """Copy pages src[i] of src_pages' pools to pages dst[i] of dst_pages' (int32)."""
+    _here("tq_pages_copy", src_pages._dev, dst_pages.refs, src, dst)
     n = src.numel()
     _check(lib().tq_pages_copy(h, src_pages._ref, dst_pages._ref, _int32(src, "src", n), _int32(dst, "dst", n), n,
                                _stream(stream)), "tq_pages_copy")

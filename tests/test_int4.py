@@ -909,3 +909,48 @@ def test_chunks_between_turboquant_encodes(libtq, d, dtype, Tnew):
     got, again = run([torch.zeros_like(q) for _ in range(20)], False)
     assert all(torch.equal(o, want[0]) for o in got) and all(torch.equal(a, b) for a, b in zip(stored, again))
     cs.close()
+
+
+def test_tensors_off_the_device_are_refused_cpu(libtq):
+    """A host pointer would be followed by a kernel: refused before anything is called (the handle is not looked at)."""
+    for dev, t in ((-1, ()), (0, (torch.zeros(1),)), (0, (None, torch.zeros(1)))):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            tq._here("call", dev, *t)
+    class OnGpu:
+        get_device = staticmethod(lambda: 0)
+
+    with pytest.raises(ValueError, match="one device"):
+        tq._one_device("call", torch.zeros(1), OnGpu())
+    assert tq._one_device("call", torch.zeros(1), None) == -1
+
+
+@gpu
+def test_tensors_off_the_device_are_refused(libtq):
+    """Index vectors, queries, vectors, outputs, workspaces and caches on the host beside caches on the GPU."""
+    d, group = 128, 64
+    cs, _, _ = _filled(d, group, 2, 2, 128, 1)
+    h, (kc, vc) = cs.h, cs.caches
+    q, out = torch.zeros((2, 1, 4, d), device="cuda"), torch.zeros((2, 1, 4, d), device="cuda")
+    x, lens = torch.zeros((2, 2, 1, d), device="cuda"), torch.tensor([5, 6], dtype=torch.int32, device="cuda")
+    ws = torch.zeros(tq.tq_attend_int4_workspace_bytes(h, 2, 1, 4, 2), dtype=torch.uint8, device="cuda")
+    host = tq.Int4Cache(d, group, 2, 2, 128, device="cpu")
+    before = [c.buf.clone() for c in cs.caches]
+    with pytest.raises(ValueError, match="one device"):
+        tq.Int4Cache(d, group, 2, 2, 128, block_table=torch.zeros((4, 2), dtype=torch.int32), pool_blocks=8)
+    good = dict(q=q, kc=kc, vc=vc, out=out, ws=ws, seq_lens=lens)
+    for name in good:
+        bad = dict(good, **{name: host if name in ("kc", "vc") else good[name].cpu()})
+        with pytest.raises(ValueError, match="current CUDA device"):
+            tq.tq_attend_int4(h, bad["q"], bad["kc"], bad["vc"], bad["out"], bad["ws"], seq_lens=bad["seq_lens"])
+    good = dict(k=x, v=x, kc=kc, vc=vc, q=q, out=out, ws=ws, pos=lens)
+    for name in good:
+        bad = dict(good, **{name: host if name in ("kc", "vc") else good[name].cpu()})
+        with pytest.raises(ValueError, match="current CUDA device"):
+            tq.tq_append_attend_int4(h, *(bad[n] for n in ("k", "v", "kc", "vc", "q", "out", "ws")), pos=bad["pos"])
+    for f in (lambda x, c, p: tq.tq_encode_int4(h, x, c, pos=p), lambda x, c, p: tq.tq_expand_int4(h, c, x, pos=p)):
+        for args in ((x.cpu(), kc, lens), (x, host, lens), (x, kc, lens.cpu())):
+            with pytest.raises(ValueError, match="current CUDA device"):
+                f(*args)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, c.buf) for a, c in zip(before, cs.caches)) and not out.any()
+    cs.close()

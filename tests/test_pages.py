@@ -457,3 +457,36 @@ def test_bulk_append_behind_a_call_that_writes_what_it_reads(libtq, d, dtype, be
         for a, b in zip(run(False), want):
             assert torch.equal(a, b)
     tq.tq_destroy(h)
+
+
+def test_pages_on_the_host_are_refused_cpu(libtq):
+    t, r = torch.full((4, 3), -1, dtype=torch.int32), torch.zeros(10, dtype=torch.int32)
+    pg = tq.Pages(t, r, 2, [(torch.zeros((10, 64), dtype=torch.uint8), 64)])
+    v, info, ws = torch.zeros(2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(4096, dtype=torch.uint8)
+    for f in (lambda: tq.tq_pages_alloc(None, pg, v, v, info, ws), lambda: tq.tq_pages_fork(None, pg, v),
+              lambda: tq.tq_pages_free(None, pg, v), lambda: tq.tq_pages_compact(None, pg, info, ws),
+              lambda: tq.tq_pages_copy(None, pg, pg, v, v)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            f()
+
+
+@gpu
+def test_vectors_on_the_host_are_refused(libtq):
+    table, refs, pools = build(3, 2, 5, 60, [300, 300, 129], share=3)
+    g = Dev(table, refs, pools, 2)
+    v, host, info = i32([0, 1, 2]), torch.zeros(3, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    for f in (lambda: tq.tq_pages_alloc(g.h, g.pages, host, v, g.info, g.ws),
+              lambda: tq.tq_pages_alloc(g.h, g.pages, v, host, g.info, g.ws),
+              lambda: tq.tq_pages_alloc(g.h, g.pages, v, v, info, g.ws),
+              lambda: tq.tq_pages_alloc(g.h, g.pages, v, v, g.info, g.ws.cpu()),
+              lambda: tq.tq_pages_fork(g.h, g.pages, host), lambda: tq.tq_pages_free(g.h, g.pages, host),
+              lambda: tq.tq_pages_compact(g.h, g.pages, info, g.ws),
+              lambda: tq.tq_pages_compact(g.h, g.pages, g.info, g.ws.cpu()),
+              lambda: tq.tq_pages_copy(g.h, g.pages, g.pages, host, v),
+              lambda: tq.tq_pages_copy(g.h, g.pages, g.pages, v, host)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            f()
+    with pytest.raises(ValueError, match="one device"):
+        tq.Pages(g.t, g.r.cpu(), 2, [])
+    assert np.array_equal(g.t.cpu().numpy(), table) and np.array_equal(g.r.cpu().numpy(), refs)
+    g.close()
