@@ -95,7 +95,7 @@ __host__ __device__ constexpr float lazy(bool one_limb) { return 15.f - room(one
 
 template <int DT>
 __device__ __forceinline__ float load_elem(const void* p, int64_t i) {
-    if constexpr (DT == TQ_F32) return __ldg(static_cast<const float*>(p) + i);
+    if constexpr (DT == TQ_F32) return static_cast<const float*>(p)[i];
     else if constexpr (DT == TQ_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
     else return __half2float(static_cast<const __half*>(p)[i]);
 }
@@ -113,7 +113,7 @@ __device__ __forceinline__ float fast_log2(float x) {
 
 // tokens of sequence b, and its chunks (at least one, so that an empty sequence's rows are written)
 __device__ __forceinline__ int64_t seq_len(const Int4AttendArgs& a, int64_t b) {
-    const int64_t n = (a.lens ? (int64_t)__ldg(a.lens + b) : a.T) + a.add;
+    const int64_t n = (a.lens ? (int64_t)a.lens[b] : a.T) + a.add;
     return n < 0 ? 0 : (n > a.Tcap ? a.Tcap : n);
 }
 template <int CH>
@@ -200,7 +200,7 @@ __device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, u
 // pool block of a block-table entry (contiguous cache: the row itself); bad: -1 and the check word
 __device__ __forceinline__ int64_t table_entry(const int32_t* table, int64_t pool, int64_t row, int* err) {
     if (!table) return row;
-    const int32_t p = __ldg(table + row);
+    const int32_t p = table[row];
     if (p < 0 || (int64_t)p >= pool) {
         atomicExch(err, 1);
         return -1;

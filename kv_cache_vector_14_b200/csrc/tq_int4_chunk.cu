@@ -101,7 +101,7 @@ enum : int {
 
 // tokens that the last row of row tile rt sees, and the tiles they take (at least one)
 __device__ __forceinline__ int64_t chunk_len(const Int4AttendArgs& a, int64_t b) {
-    const int64_t n = (a.lens ? (int64_t)__ldg(a.lens + b) : a.T) + a.add;
+    const int64_t n = (a.lens ? (int64_t)a.lens[b] : a.T) + a.add;
     return n < 0 ? 0 : (n > a.Tcap ? a.Tcap : n);
 }
 template <int ROWS, int TT>
@@ -242,7 +242,7 @@ __device__ __forceinline__ void load_raw(const void* p, int64_t at, bool vec, bo
     if (vec) {
 #pragma unroll
         for (int i = 0; i < kN / 4; ++i) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(s) + i);
+            const uint4 u = reinterpret_cast<const uint4*>(s)[i];
             w[4 * i] = u.x; w[4 * i + 1] = u.y; w[4 * i + 2] = u.z; w[4 * i + 3] = u.w;
         }
     } else if constexpr (DT == TQ_F32) {

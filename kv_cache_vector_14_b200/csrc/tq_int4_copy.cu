@@ -52,7 +52,7 @@ __device__ __forceinline__ Spot spot(const Int4CopyArgs& a, const Int4Side& sd, 
     const uint32_t b = fdiv(bh, a.fdH);
     const uint32_t hh = bh - b * (uint32_t)a.Hkv;
     r.xoff = (int64_t)b * a.sb + (int64_t)hh * a.sh + (int64_t)tt * a.st;
-    const int64_t t = (a.pos ? (int64_t)__ldg(a.pos + b) : a.t0) + tt;
+    const int64_t t = (a.pos ? (int64_t)a.pos[b] : a.t0) + tt;
     r.tau = (int)(t & 63);
     r.blk = nullptr;
     if (t < 0 || t >= a.Tcap) {
@@ -122,7 +122,7 @@ __device__ __forceinline__ void load16(const void* x, int64_t off, bool vec, uin
     if (vec) {
 #pragma unroll
         for (int i = 0; i < kRaw<DT> / 4; ++i) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+            const uint4 v = reinterpret_cast<const uint4*>(p)[i];
             w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
         }
     } else if constexpr (DT == TQ_F32) {

@@ -174,11 +174,13 @@ struct DecArgs {
 #ifdef __CUDACC__
 // Block index of logical block lb of sequence bh (= b * Hkv + h): bh * NB + lb
 // for a contiguous cache, the block table's entry for a paged one.  An entry
-// outside the pool sets the check word and gives -1.
+// outside the pool sets the check word and gives -1.  (A plain load, as of everything that a
+// kernel still running when this one started may write: __ldg promises that the bytes do not
+// change while the kernel lives, and may be moved above pdl_wait.)
 __device__ __forceinline__ int64_t cache_block(const int32_t* table, int64_t pool, int64_t NB, int64_t bh,
                                                int64_t lb, int* err) {
     if (!table) return bh * NB + lb;
-    const int32_t p = __ldg(table + bh * NB + lb);
+    const int32_t p = table[bh * NB + lb];
     if (p < 0 || (int64_t)p >= pool) {
         atomicExch(err, 1);
         return -1;

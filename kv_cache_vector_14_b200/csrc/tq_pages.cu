@@ -30,7 +30,7 @@ __global__ void __launch_bounds__(256) tq_pages_free_kernel(const PagesArgs a, c
     const int64_t n = a.B * a.Hkv * a.NB;
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
         const int64_t row = i / a.NB, lb = i - row * a.NB;
-        const int64_t k = __ldg(keep + row / a.Hkv);
+        const int64_t k = keep[row / a.Hkv];
         if (lb * kBlockT < k) continue;
         const int32_t e = a.table[i];
         if (e < 0) continue;
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(256) tq_pages_fork_kernel(const PagesArgs a, c
     __syncthreads();
     if (lb >= a.NB) return;
     for (int64_t b = y; b < a.B; b += 256 / kForkCols) {
-        const int64_t p = __ldg(parent + b);
+        const int64_t p = parent[b];
         if (p == b) continue;
         if (p < -1 || p >= a.B) {
             atomicExch(a.err, 1);
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kPlan) tq_pages_alloc_kernel(const PagesArgs a
     auto requests = [&](auto f) {
         for (int64_t row = r0; row < r1; ++row) {
             const int64_t b = row / a.Hkv;
-            int64_t l = __ldg(lo + b), h = __ldg(hi + b);
+            int64_t l = lo[b], h = hi[b];
             if (l < 0 || h > a.NB * kBlockT) {
                 atomicExch(a.err, 1);
                 l = l < 0 ? 0 : l;
