@@ -353,7 +353,8 @@ TQ_API size_t tq_attend_int4_workspace_bytes(const tq_handle* h, int64_t B, int6
  * values carry at least 22 bits for fp32 and fp16 calls.  bf16 calls round the
  * weights times the value scales to fp16 (2^-11, against 2^-8 of their output),
  * and with more than 8 query rows per kv head (head_dim 64 and 128) the
- * expanded keys and values too.
+ * expanded keys and values too, to 65504 at most (a group whose maximum is
+ * clipped there may stand for up to 64 more).
  * Supported: any Hq/Hkv, B < 2^31, Lq * Hq / Hkv < 2^31, Hkv * row groups <
  * 2^31 (row groups: query rows per kv head / 4, rounded up); contiguous or
  * paged caches.  ws: 256-byte aligned, at least

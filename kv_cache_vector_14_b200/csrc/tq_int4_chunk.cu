@@ -7,7 +7,7 @@
 // block.  A tile is expanded once into shared memory and serves all rows:
 //   S[128 rows][64] = Q K^T     (A: Q in shared memory, B: K, both K-major)
 //   O[128 rows][D] += P V       (A: P in tensor memory over S, B: V, MN-major)
-// The expanded values zero + scale c are rounded to fp16, bf16 and fp16 queries enter
+// The expanded values zero + scale c are rounded to fp16 (65504 at most), bf16 and fp16 queries enter
 // exactly (scaled by a power of two per row), P is fp16.  For bf16 that is one product
 // each (NL = 1): those roundings are 2^-11 relative and the output's own is 2^-8.  For
 // fp16 and fp32 they would show, so K, V and P (and fp32 Q) are kept as fp16 hi + lo
@@ -41,6 +41,7 @@
 // group at the end (a row sees a prefix of the tokens, so the first one decides).
 // So a NaN does not reach the rows for which it is masked, as a product 0 NaN would.
 #include <climits>
+#include <type_traits>
 
 #include "tq_frag.cuh"
 #include "tq_int4.h"
@@ -190,8 +191,10 @@ __host__ __device__ constexpr int word_value(int p) { return (p >> 1) + 4 * (p &
 
 __device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 
-// the eight values of word w, zero + scale c, as four fp16 pairs (hi; with NL = 2 lo too)
-template <int NL>
+// the eight values of word w, zero + scale c, as four fp16 pairs (hi; with NL = 2 lo too).  TOP:
+// a value may lie above 65504 (scale is a rounded number: by 15 scale 2^-11 <= 64); hi stays at
+// 65504, which the mma needs finite, and lo carries the rest.
+template <int NL, bool TOP>
 __device__ __forceinline__ void expand_word(uint32_t w, __half2 s2, __half2 z2, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
     const uint32_t w8 = w >> 8;
     const __half2 m1024 = as_h2(0xe400e400u), sixteenth = as_h2(0x2c002c00u), m64 = as_h2(0xd400d400u);
@@ -201,7 +204,8 @@ __device__ __forceinline__ void expand_word(uint32_t w, __half2 s2, __half2 z2, 
         // 1024 + c (or 1024 + 16 c) as fp16, then c exactly, then one rounding of zero + scale c
         const __half2 c = (r & 1) ? __hfma2(as_h2((v & 0x00f000f0u) | 0x64006400u), sixteenth, m64)
                                   : __hadd2(as_h2((v & 0x000f000fu) | 0x64006400u), m1024);
-        const __half2 h = __hfma2(c, s2, z2);
+        __half2 h = __hfma2(c, s2, z2);
+        if constexpr (TOP) h = __hmin2_nan(h, as_h2(0x7bff7bffu));
         hi[r] = h2_bits(h);
         if constexpr (NL == 2) {
             const float2 cf = __half22float2(c), hf = __half22float2(h);
@@ -668,28 +672,30 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             if (rare) {                                        // (after the wait: it bounds how far ahead marks are made)
 #pragma unroll
                 for (int it = 0; it < 2 * kItems; ++it) {
-                    if (it >= kItems && ((bits[it] & 0x7c00u) == 0x7c00u || (bits[it] & 0x7c000000u) == 0x7c000000u)) {
-                        bits[it] = 0u;
-                        atomicMin(&sBad[4 * (seg & 7) + gam], (int)tok0 + tau0 + 32 * (it % kItems));
+                    if ((bits[it] & 0x7c00u) == 0x7c00u || (bits[it] & 0x7c000000u) == 0x7c000000u) {
+                        bits[it] = it < kItems ? 0x7e007e00u : 0u;     // a key: NaN, whatever its codes
+                        if (it >= kItems) atomicMin(&sBad[4 * (seg & 7) + gam], (int)tok0 + tau0 + 32 * (it % kItems));
                     }
-                    // the largest value stays finite in fp16
-                    if (fmaf(15.f, __low2float(as_h2(bits[it])), __high2float(as_h2(bits[it]))) > 65504.f) bits[it] -= 1u;
                 }
             }
             uint8_t* buf = sm + bf * C::kBuf;
+            auto build = [&](auto top) {
 #pragma unroll
-            for (int it = 0; it < 2 * kItems; ++it) {
-                const __half2 s2 = __low2half2(as_h2(bits[it])), z2 = __high2half2(as_h2(bits[it]));
-                const uint32_t wd[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
-                uint8_t* op = buf + (it / kItems) * NL * C::kTile + 32 * (it % kItems) * 128;    // (32 rows: 4 atoms of 1024 bytes)
+                for (int it = 0; it < 2 * kItems; ++it) {
+                    const __half2 s2 = __low2half2(as_h2(bits[it])), z2 = __high2half2(as_h2(bits[it]));
+                    const uint32_t wd[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
+                    uint8_t* op = buf + (it / kItems) * NL * C::kTile + 32 * (it % kItems) * 128;    // (32 rows: 4 atoms of 1024 bytes)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t h[4], l[4];
-                    expand_word<NL>(wd[i], s2, z2, h, l);
-                    *reinterpret_cast<uint4*>(op + at[i]) = make_uint4(h[0], h[1], h[2], h[3]);
-                    if constexpr (NL == 2) *reinterpret_cast<uint4*>(op + C::kTile + at[i]) = make_uint4(l[0], l[1], l[2], l[3]);
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t h[4], l[4];
+                        expand_word<NL, decltype(top)::value>(wd[i], s2, z2, h, l);
+                        *reinterpret_cast<uint4*>(op + at[i]) = make_uint4(h[0], h[1], h[2], h[3]);
+                        if constexpr (NL == 2) *reinterpret_cast<uint4*>(op + C::kTile + at[i]) = make_uint4(l[0], l[1], l[2], l[3]);
+                    }
                 }
-            }
+            };
+            build(std::false_type{});
+            if (rare) build(std::true_type{});     // again over it (512-token step: as an else branch 349 us, this way 345)
             fence_proxy_async();           // operands for the tensor core; the slot's reads before its next copies
             mbar_arrive(bar(kBarReady + bf));
             mbar_arrive(bar(kBarSlot + slot));

@@ -954,3 +954,18 @@ def test_tensors_off_the_device_are_refused(libtq):
     torch.cuda.synchronize()
     assert all(torch.equal(a, c.buf) for a, c in zip(before, cs.caches)) and not out.any()
     cs.close()
+
+
+@gpu
+@pytest.mark.parametrize("d,group", [(64, 32), (64, 64), (128, 64), (128, 128)])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("G,Lq", [(4, 1), (4, 10), (4, 80)])
+def test_values_at_the_fp16_limit(libtq, d, group, dtype, G, Lq):
+    """Groups clipped at 65504, whose zero + 15 scale may lie above it, as keys and as values: the same at 4, 40 and
+    320 query rows."""
+    rng = np.random.default_rng(d + group)
+    T = 400
+    kx, vx = (rng.standard_normal((1, 2, T, d)).astype(np.float32) * 5e4 for _ in range(2))
+    top = U.grid(vx[0, 0], group)
+    assert (top > 65504).any()
+    check_attend(d, group, dtype, kx, vx, rng.standard_normal((1, Lq, 2 * G, d)).astype(np.float32), T, 1e-6, limit=True)
