@@ -549,6 +549,10 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             if (!failed && !warp_wait(bar(kBarSeg), (uint32_t)(seg & 1))) failed = true;
             tc_fence_after();
             if (!any) mref = -INFINITY;
+            if (lim == 0) {                                    // sees nothing: zeros, whatever its query
+                mref = -INFINITY;
+                lsum = 0.f;
+            }
             // groups with a non-finite pair on a token that this row sees
             uint32_t bad = 0;
 #pragma unroll

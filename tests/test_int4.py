@@ -969,3 +969,22 @@ def test_values_at_the_fp16_limit(libtq, d, group, dtype, G, Lq):
     top = U.grid(vx[0, 0], group)
     assert (top > 65504).any()
     check_attend(d, group, dtype, kx, vx, rng.standard_normal((1, Lq, 2 * G, d)).astype(np.float32), T, 1e-6, limit=True)
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("G,Lq", [(1, 4), (4, 30), (4, 50)])
+def test_rows_that_see_nothing_are_zero_whatever_their_query(libtq, dtype, G, Lq):
+    """A sequence shorter than its queries: the first rows see no token and give zeros, NaN or infinite queries too;
+    a NaN in a row that sees tokens is its own."""
+    cs, _, _ = _filled(128, 64, 2, 1, 128, 5)
+    q = torch.randn((2, Lq, G, 128), device="cuda").to(TYPES[dtype])
+    q[0, 0, 0, 7], q[0, 1, G - 1, 100], q[1, :, :, 3] = float("nan"), float("inf"), float("nan")
+    q[0, Lq - 1, 0, 0] = float("nan")
+    out = torch.full_like(q, 3.0)
+    ws = torch.zeros(tq.tq_attend_int4_workspace_bytes(cs.h, 2, Lq, G, 1), dtype=torch.uint8, device="cuda")
+    tq.tq_attend_int4(cs.h, q, *cs.caches, out, ws, seq_lens=torch.tensor([2, 0], dtype=torch.int32, device="cuda"),
+                      scale=0.1)
+    assert not out[0, :Lq - 2].any() and not out[1].any()
+    assert torch.isnan(out[0, Lq - 1, 0]).all() and torch.isfinite(out[0, Lq - 2]).all()
+    cs.close()
