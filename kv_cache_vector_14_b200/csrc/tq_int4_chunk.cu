@@ -578,10 +578,8 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             const float f0 = m0 == -INFINITY || failed ? 0.f : fast_exp2(m0 - mm);
             const float f1 = m1 == -INFINITY || failed ? 0.f : fast_exp2(m1 - mm);
             const float f2 = mrun == -INFINITY || failed ? 0.f : fast_exp2(mrun - mm);
-            float L = f2 * lrun;
-            if (f0 != 0.f) L = fmaf(f0, l0, L);
-            if (f1 != 0.f) L = fmaf(f1, l1, L);
-            if (mm == -INFINITY) L = 0.f;
+            // (a sum that is NaN stays in L though its factor is 0; one without a token is 0)
+            const float L = mm == -INFINITY ? 0.f : fmaf(f1, l1, fmaf(f0, l0, f2 * lrun));
             const float inv = whole && mm != -INFINITY ? 1.f / L : 1.f;
             float* part = a.part_acc + (slot - ur) * D + ur;   // [D][ROWS]: the lanes of a store are neighbours
 #pragma unroll 1

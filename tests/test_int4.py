@@ -988,3 +988,26 @@ def test_rows_that_see_nothing_are_zero_whatever_their_query(libtq, dtype, G, Lq
     assert not out[0, :Lq - 2].any() and not out[1].any()
     assert torch.isnan(out[0, Lq - 1, 0]).all() and torch.isfinite(out[0, Lq - 2]).all()
     cs.close()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("Lq", [1, 10, 40])
+def test_nan_key_is_not_lost_beside_far_larger_scores(libtq, dtype, Lq):
+    """A NaN score makes the row NaN although the other tokens of its tile have no weight beside those of the next
+    tile (scores 256 and more apart).  Many sequences, so that one CTA holds both tiles."""
+    d, B, G, T = 128, 300, 4, 192
+    rng = np.random.default_rng(Lq)
+    cs = Case(d, 64, B, 1, T)
+    k, v = rand(rng, (B, 1, T, d)) * np.float32(0.05), rand(rng, (B, 1, T, d), False)
+    k[:, :, 64:128] = 1.0                                    # q = 1: scores 128 scale
+    k[::2, 0, 5, 70] = np.nan
+    for c, x in zip(cs.caches, (k, v)):
+        tq.tq_encode_int4(cs.h, to_gpu(x, "f32"), c)
+    q = torch.ones((B, Lq, G, d), device="cuda", dtype=TYPES[dtype])
+    out = torch.zeros_like(q)
+    ws = torch.zeros(tq.tq_attend_int4_workspace_bytes(cs.h, B, Lq, G, 1), dtype=torch.uint8, device="cuda")
+    tq.tq_attend_int4(cs.h, q, *cs.caches, out, ws, T=T, scale=2.0)
+    bad = torch.isnan(out)
+    assert bad[::2].all() and not bad[1::2].any()
+    cs.close()
