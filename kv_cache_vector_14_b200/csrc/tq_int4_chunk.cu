@@ -191,11 +191,12 @@ __host__ __device__ constexpr int word_value(int p) { return (p >> 1) + 4 * (p &
 
 __device__ __forceinline__ __half2 as_h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 
-// the eight values of word w, zero + scale c, as four fp16 pairs (hi; with NL = 2 lo too).  TOP:
-// a value may lie above 65504 (scale is a rounded number: by 15 scale 2^-11 <= 64); hi stays at
-// 65504, which the mma needs finite, and lo carries the rest.
+// The eight values of word w, zero + scale c, as four fp16 pairs: hi, and with NL = 2 lo, what the
+// value lies above it.  The scale is a rounded number, so the top of a group may lie above 65504, by
+// 15 scale 2^-11 <= 64, where the mma needs a finite hi.  NL = 1: TOP keeps it at 65504.  NL = 2: s2
+// is one unit lower then, and lo, from the exact pair, carries the difference (at most 120).
 template <int NL, bool TOP>
-__device__ __forceinline__ void expand_word(uint32_t w, __half2 s2, __half2 z2, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
+__device__ __forceinline__ void expand_word(uint32_t w, __half2 s2, __half2 z2, __half2 pair, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
     const uint32_t w8 = w >> 8;
     const __half2 m1024 = as_h2(0xe400e400u), sixteenth = as_h2(0x2c002c00u), m64 = as_h2(0xd400d400u);
 #pragma unroll
@@ -209,7 +210,7 @@ __device__ __forceinline__ void expand_word(uint32_t w, __half2 s2, __half2 z2, 
         hi[r] = h2_bits(h);
         if constexpr (NL == 2) {
             const float2 cf = __half22float2(c), hf = __half22float2(h);
-            const float s = __low2float(s2), z = __low2float(z2);
+            const float s = __low2float(pair), z = __high2float(pair);
             lo[r] = h2_bits(__floats2half2_rn(fmaf(cf.x, s, z) - hf.x, fmaf(cf.y, s, z) - hf.y));
         }
     }
@@ -658,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             const int valid = inside < TT ? (int)(inside > 0 ? inside : 0) : TT;           // tokens inside the sequence
             // items: K, then V
             uint4 v[2 * kItems];
-            uint32_t bits[2 * kItems];
+            uint32_t bits[2 * kItems], high[2 * kItems];       // pairs; and those of hi (see expand_word)
             bool rare = false;
 #pragma unroll
             for (int it = 0; it < 2 * kItems; ++it) {
@@ -669,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                 if (tau0 + dt >= valid) bits[it] = 0u;         // behind the sequence anything may stand
                 // a scale of 2^11 or more, a zero of 2^15 or more, infinity or NaN
                 rare |= (bits[it] & 0x7fffu) >= 0x6800u || (bits[it] & 0x7fff0000u) >= 0x78000000u;
+                high[it] = bits[it];
             }
             if (j >= C::kBufs && !mbar_wait_bounded(bar(kBarFree + bf), (uint32_t)(bfp ^ 1))) { failed = true; break; }
             if (rare) {                                        // (after the wait: it bounds how far ahead marks are made)
@@ -678,26 +680,28 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
                         bits[it] = it < kItems ? 0x7e007e00u : 0u;     // a key: NaN, whatever its codes
                         if (it >= kItems) atomicMin(&sBad[4 * (seg & 7) + gam], (int)tok0 + tau0 + 32 * (it % kItems));
                     }
+                    high[it] = bits[it];
+                    if (NL == 2 && fmaf(15.f, __low2float(as_h2(bits[it])), __high2float(as_h2(bits[it]))) > 65504.f) high[it] -= 1u;
                 }
             }
             uint8_t* buf = sm + bf * C::kBuf;
             auto build = [&](auto top) {
 #pragma unroll
                 for (int it = 0; it < 2 * kItems; ++it) {
-                    const __half2 s2 = __low2half2(as_h2(bits[it])), z2 = __high2half2(as_h2(bits[it]));
+                    const __half2 s2 = __low2half2(as_h2(high[it])), z2 = __high2half2(as_h2(high[it]));
                     const uint32_t wd[4] = {v[it].x, v[it].y, v[it].z, v[it].w};
                     uint8_t* op = buf + (it / kItems) * NL * C::kTile + 32 * (it % kItems) * 128;    // (32 rows: 4 atoms of 1024 bytes)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t h[4], l[4];
-                        expand_word<NL, decltype(top)::value>(wd[i], s2, z2, h, l);
+                        expand_word<NL, decltype(top)::value>(wd[i], s2, z2, as_h2(bits[it]), h, l);
                         *reinterpret_cast<uint4*>(op + at[i]) = make_uint4(h[0], h[1], h[2], h[3]);
                         if constexpr (NL == 2) *reinterpret_cast<uint4*>(op + C::kTile + at[i]) = make_uint4(l[0], l[1], l[2], l[3]);
                     }
                 }
             };
             build(std::false_type{});
-            if (rare) build(std::true_type{});     // again over it (512-token step: as an else branch 349 us, this way 345)
+            if (NL == 1 && rare) build(std::true_type{});      // again over it (512-token step 345 us; as an else branch 349)
             fence_proxy_async();           // operands for the tensor core; the slot's reads before its next copies
             mbar_arrive(bar(kBarReady + bf));
             mbar_arrive(bar(kBarSlot + slot));
