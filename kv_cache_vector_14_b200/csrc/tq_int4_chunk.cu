@@ -76,10 +76,14 @@ struct Ch {
     static_assert(kOffRing % 16 == 0 && kOffBar % 8 == 0 && kOffScan % 8 == 0, "alignment");
     static_assert(kSmem <= 227 * 1024, "shared memory per CTA");
     // tensor memory columns
-    // Tiles of a segment.  The tensor core truncates its sums, and 12 additions per tile onto an fp32
-    // O cost an fp32 call 3e-5 of its result in 225 tiles; so O is taken out every 16 of a stream's tiles and added
-    // up in the workspace, correctly rounded.  (16-bit outputs do not show it.)
-    static constexpr int kSegTiles = QL == 1 ? INT_MAX / 2 : MT == 2 ? 16 : 32;
+    // Tiles of a segment.  The tensor core truncates its sums: an O of values with a mean loses up to
+    // 5e-7 of itself per tile (3.5e-4 in 1100).  So O is taken out after 16 (fp32: 8e-6 of the result)
+    // or 256 (fp16: 1.3e-4, a quarter of the half step) of a stream's tiles and added up in the workspace,
+    // correctly rounded; a take-out costs 20 to 40 us (loads, stores and a drained pipeline).  bf16 calls go without: their half step is reached in some 10000 tiles of one
+    // CTA (include/tq.h says so), and the code alone costs the 512-token step 3 %.
+    static constexpr bool kTakeOut = NL == 2;
+    static constexpr int kSegStream = !kTakeOut ? INT_MAX / 4 : QL == 2 ? 16 : 256;
+    static constexpr int kSegTiles = MT == 2 ? kSegStream : 2 * kSegStream;
     static constexpr int kX = 0;                              // S / P of stream x, buffer b at TT (2 x + b)
     static constexpr int kO = 4 * TT;                         // O of stream x at kO + D x
     static_assert(kO + 2 * D <= 512, "tensor memory");
@@ -411,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             const int k0 = w.k, left = w.nt - w.k;
             const int most = left < C::kSegTiles ? left : C::kSegTiles;
             const int j1 = j + most < J ? j + most : J;
-            if (QL == 1 || !cont) ubegins = k0 == 0;
+            if (!C::kTakeOut || !cont) ubegins = k0 == 0;
             const int ur = MT == 2 ? 128 * x + r : r;         // row of the unit
             const int64_t grow = (int64_t)w.rt * ROWS + ur;
             const bool rvalid = grow < a.rows;
@@ -423,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             const int lim = lim64 < 0 ? 0 : (int)lim64;
             // query operand: the row scaled by a power of two (largest element in [2^14, 2^15));
             // position p of a word's eight holds value word_value(p), as in the expanded operands
-            if (QL == 1 || !cont) {
+            if (!C::kTakeOut || !cont) {
                 // (all loads at once; 64 registers with MT = 2)
                 constexpr int kRegs = kCols * (DT == TQ_F32 ? 4 : 2) / 4;
                 uint32_t raw_q[kRegs];
@@ -583,32 +587,55 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             const float L = mm == -INFINITY ? 0.f : fmaf(f1, l1, fmaf(f0, l0, f2 * lrun));
             const float inv = whole && mm != -INFINITY ? 1.f / L : 1.f;
             float* part = a.part_acc + (slot - ur) * D + ur;   // [D][ROWS]: the lanes of a store are neighbours
-#pragma unroll 1
-            for (int c0 = 0; c0 < kCols; c0 += 8) {
-                const int col = col0 + c0;
+            // eight columns of this segment, in value order
+            auto take = [&](int col, float (&v)[8]) {
                 uint32_t o0[8], o1[8];
                 tc_ld8(tl + C::kO + (MT == 2 ? D * x : 0) + col, o0);
                 if constexpr (MT == 1) tc_ld8(tl + C::kO + D + col, o1);
                 const bool poison = (bad >> (col / GRP)) & 1u; // (a run of 8 lies in one group)
-                if (!rvalid) continue;
-                float v[8];
 #pragma unroll
                 for (int cc = 0; cc < 8; ++cc) {
                     float y = f0 != 0.f ? __uint_as_float(o0[cc]) * f0 : 0.f;
                     if constexpr (MT == 1) y = f1 != 0.f ? fmaf(__uint_as_float(o1[cc]), f1, y) : y;
                     v[word_value(cc)] = poison && mm != -INFINITY ? __uint_as_float(0x7fc00000u) : y;
                 }
-                if (QL == 2 && cont) {                         // what this thread stored there (0 NaN stays NaN)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] = fmaf(part[(int64_t)(col + e) * ROWS], f2, v[e]);
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] *= inv;
+            };
+            auto put = [&](int col, const float (&v)[8]) {
+                if (!rvalid) return;
                 if (whole) {
                     store8<DT>(a.out, qrow * D + col, a.vec16, v);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) part[(int64_t)(col + e) * ROWS] = v[e];
+                }
+            };
+            if (C::kTakeOut && cont) {
+                // beside what this thread stored there (0 NaN stays NaN), in a loop of its own: one loop for
+                // both cost 8 % of a call that takes nothing out.  32 columns in flight, 8 where more
+                // registers cost the tiles' loop (512-token step, fp32, head_dim 128: 2640 -> 2525 us)
+                constexpr int kStep = D == 128 ? 32 : 8;
+#pragma unroll 1
+                for (int c0 = 0; c0 < kCols; c0 += kStep) {
+                    float pv[kStep];
+#pragma unroll
+                    for (int e = 0; e < kStep; ++e) pv[e] = rvalid ? part[(int64_t)(col0 + c0 + e) * ROWS] : 0.f;
+#pragma unroll
+                    for (int q = 0; q < kStep / 8; ++q) {
+                        float v[8];
+                        take(col0 + c0 + 8 * q, v);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] = fmaf(pv[8 * q + e], f2, v[e]) * inv;
+                        put(col0 + c0 + 8 * q, v);
+                    }
+                }
+            } else {
+#pragma unroll 1
+                for (int c0 = 0; c0 < kCols; c0 += 8) {
+                    float v[8];
+                    take(col0 + c0, v);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] *= inv;
+                    put(col0 + c0, v);
                 }
             }
             if (rvalid && !whole && (MT == 2 || x == 0)) {
@@ -626,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) tq_int4_chunk_kernel(const __grid
             tc_fence_before();
             soft_or(false);
             tc_fence_after();
-            if constexpr (QL == 2) {
+            if constexpr (C::kTakeOut) {
                 cont = !ends;
                 mrun = mm;
                 lrun = L;

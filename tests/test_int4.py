@@ -1011,3 +1011,43 @@ def test_nan_key_is_not_lost_beside_far_larger_scores(libtq, dtype, Lq):
     bad = torch.isnan(out)
     assert bad[::2].all() and not bad[1::2].any()
     cs.close()
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_chunk_sums_over_a_long_context(libtq, dtype):
+    """Units enough that one CTA walks a whole unit of 1100 tiles, values with a mean of 1: the mean error of the
+    outputs shows a drift of the sums, which the tensor core truncates, by up to 5.2e-7 a tile.  fp16 sums are taken
+    out every 256 tiles (1.33e-4 < 2^-12.8, a quarter of the half step); fp32: 16 tiles (8.3e-6), 2^-17
+    and the 2^-18 allowed everywhere; bf16 is not taken out: an eighth of the half step, 2^-11.  Beside it the mean
+    of n roundings of half a step at most: 6 standard deviations.  The reference is rounded too: the grid is twice
+    as fine below 1 as above, so roundings around a mean of 1 have a mean of their own, the same on both sides."""
+    d, group, G, T = 128, 64, 8, 70400
+    Lq = 148 * 256 // G
+    h = tq.tq_init(d, 0)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    k = torch.randn((1, 1, T, d), generator=gen, device="cuda")
+    v = 1.0 + 0.3 * torch.randn((1, 1, T, d), generator=gen, device="cuda")
+    caches = [tq.Int4Cache(d, group, 1, 1, T) for _ in range(2)]
+    back = [torch.empty_like(k) for _ in range(2)]
+    for x, c, b in zip((k, v), caches, back):
+        tq.tq_encode_int4(h, x, c)
+        tq.tq_expand_int4(h, c, b)
+    q = (2 * torch.randn((1, Lq, G, d), generator=gen, device="cuda")).to(TYPES[dtype])
+    out = torch.zeros_like(q)
+    ws = torch.zeros(tq.tq_attend_int4_workspace_bytes(h, 1, Lq, G, 1), dtype=torch.uint8, device="cuda")
+    tq.tq_attend_int4(h, q, *caches, out, ws, T=T, scale=d ** -0.5)
+    assert tq.tq_device_status(h) == tq.TQ_OK
+    kd, vd = (b[0, 0].double() for b in back)
+    rel = []
+    for i in range(0, Lq, 97):
+        n = T - Lq + 1 + i
+        p = torch.softmax(q[0, i].double() @ kd[:n].T * d ** -0.5, -1)
+        ref = p @ vd[:n]
+        rel.append((out[0, i].double() - ref.to(out.dtype).double()) / ref)
+    rel = torch.cat(rel)
+    half = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[dtype]
+    drift = {"f32": 2.0 ** -17, "f16": 2.0 ** -12.8, "bf16": 2.0 ** -11}[dtype]
+    noise = 2.0 ** -10 if dtype == "bf16" else 2.0 ** -18             # the rounded operands', of either sign
+    assert abs(float(rel.mean())) <= drift + 2.0 ** -18 + 6 * (half + noise) / (3 * rel.numel()) ** 0.5
+    tq.tq_destroy(h)
