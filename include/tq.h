@@ -352,12 +352,13 @@ TQ_API size_t tq_attend_int4_workspace_bytes(const tq_handle* h, int64_t B, int6
  * statistics are fp32 (integer products exact); queries, keys, weights and
  * values carry at least 22 bits for fp32 and fp16 calls.  bf16 calls round the
  * weights times the value scales to fp16 (2^-11, against 2^-8 of their output),
- * and with more than 8 query rows per kv head (head_dim 64 and 128) the
+ * and with more than 16 query rows per kv head (head_dim 64 and 128) the
  * expanded keys and values too, to 65504 at most (a group whose maximum is
  * clipped there may stand for up to 64 more).
- * Those calls sum on the tensor core, which truncates: values with a mean come
- * out low by up to 8e-6 (fp32) or 1.3e-4 (fp16) of it however long the context,
- * in bf16 calls by 3e-4 per 1000 blocks of 64 tokens that one SM walks.
+ * Those calls, and fp32 and fp16 ones of more than 32 rows, sum all tokens on
+ * the tensor core, which truncates: values with a mean come out low by up to
+ * 8e-6 (fp32) or 1.3e-4 (fp16) of it however long the context, in bf16 calls by
+ * 3e-4 per 1000 blocks of 64 tokens that one SM walks.
  * Supported: any Hq/Hkv, B < 2^31, Lq * Hq / Hkv < 2^31, Hkv * row groups <
  * 2^31 (row groups: query rows per kv head / 4, rounded up); contiguous or
  * paged caches.  ws: 256-byte aligned, at least

@@ -900,10 +900,27 @@ cudaError_t launch_g(tq_dtype dt, const Int4AttendArgs& a, int num_sms, cudaStre
 
 }  // namespace
 
-// 256-row units where there are more than 128 rows and two row tiles' query limbs fit into
-// shared memory (fp32 at head_dim 128: 128 KB of them beside 128 KB of operands do not)
+// Split kernel (units of 8 rows, each reading its cache) or chunk kernel (128 rows at a time, used or
+// not), and one or two row tiles a unit.  Attention, us, 16 sequences of 4000 tokens / one of 40960, 8 kv
+// heads:
+//   rows            12        16        24        32        64
+//   d 128 bf16 split  62 / 43   63 / 43   89 / 57  115 / 70  214 / 123
+//              chunk  67 / 62   68 / 61   68 / 62   67 / 62   67 / 63
+//         fp16 split  69 / 47   70 / 48  100 / 64  129 / 78  242 / 139
+//              chunk 211 / 148 215 / 147 219 / 151 223 / 154 237 / 163
+//         fp32 split  74 / 50   75 / 51  107 / 68  138 / 85  262 / 152
+//              chunk 244 / 163 252 / 164 258 / 166 261 / 169 271 / 175
+//   d 64  bf16 split  46 / 32   47 / 33   65 / 43   83 / 52  154 / 90
+//              chunk  53 / 54   53 / 53   53 / 54   54 / 54   55 / 54
+//         fp16 split  49 / 34   50 / 35   69 / 45   88 / 55  164 / 96
+//              chunk 106 / 84  107 / 84  111 / 86  116 / 88  129 / 98
+// so the chunk kernel takes over above 16 rows of bf16 and above 32 of the others.  256-row units above
+// 128 rows, against 128-row ones: d 128 bf16 132 rows 96 / 89 (119 / 84), 512 rows 174 / 122 (219 / 138),
+// 2048 rows 584 / 340 (769 / 482); fp16 132 rows 322 / 202 (449 / 289); d 64 bf16 132 rows 75 / 70 (92 / 70);
+// where two row tiles' query limbs fit into shared memory (fp32 at head_dim 128: 128 KB of them beside
+// 128 KB of operands do not).
 int int4_slot_rows(int d, tq_dtype dt, int rows) {
-    if (d > 128 || rows <= 8) return 8;
+    if (d > 128 || rows <= (dt == TQ_BF16 ? 16 : 32)) return 8;
     return rows > 128 && !(d == 128 && dt == TQ_F32) ? 256 : 128;
 }
 

@@ -1051,3 +1051,16 @@ def test_chunk_sums_over_a_long_context(libtq, dtype):
     noise = 2.0 ** -10 if dtype == "bf16" else 2.0 ** -18             # the rounded operands', of either sign
     assert abs(float(rel.mean())) <= drift + 2.0 ** -18 + 6 * (half + noise) / (3 * rel.numel()) ** 0.5
     tq.tq_destroy(h)
+
+
+@gpu
+@pytest.mark.parametrize("d,group", [(64, 32), (128, 64)])
+@pytest.mark.parametrize("dtype,rows", [("bf16", 16), ("bf16", 17), ("f16", 32), ("f16", 33), ("f32", 32), ("f32", 33)])
+def test_rows_on_both_sides_of_the_kernels_border(libtq, d, group, dtype, rows):
+    """The last row count of the split kernel and the first of the chunk kernel, one unit cut over many CTAs and short
+    sequences; the workspace holds whatever the queries' type."""
+    run_attend(d, group, dtype, 1, 2, [6000, 70, rows - 3, 0], Lq=rows, seed=rows)
+    h = tq.tq_init(d, 0)
+    sizes = [tq.tq_attend_int4_workspace_bytes(h, 1, n, 1, 1) for n in (8, 16, 17, 32, 33, 129)]
+    assert sizes == sorted(sizes)
+    tq.tq_destroy(h)
