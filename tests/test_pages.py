@@ -490,3 +490,76 @@ def test_vectors_on_the_host_are_refused(libtq):
         tq.Pages(g.t, g.r.cpu(), 2, [])
     assert np.array_equal(g.t.cpu().numpy(), table) and np.array_equal(g.r.cpu().numpy(), refs)
     g.close()
+
+
+@gpu
+@pytest.mark.parametrize("pool", [4000, 2500])
+def test_alloc_many_blocks_per_row(libtq, pool):
+    """A prompt's pages: hundreds of blocks of few rows, some shared, from an empty table and behind a prefix; and
+    the same where the pool runs out."""
+    Hkv, NB = 2, 600
+    table, refs, pools = build(3, Hkv, NB, pool, [5000, 5000, 0], seed=pool, share=70, sizes=(64, 32))
+    m, g = Model(table, refs, pools, Hkv), Dev(table, refs, pools, Hkv)
+    for lo, hi in (([4000, 5000, 0], [30000, 5001, 38400]), ([0, 0, 0], [64 * NB, 64, 38400])):
+        want = m.alloc(lo, hi)
+        tq.tq_pages_alloc(g.h, g.pages, i32(lo), i32(hi), g.info, g.ws)
+        g.same(m)
+        assert g.info.tolist() == want
+    assert (want[1] > 0) == (pool == 2500)
+    g.close()
+
+
+@gpu
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("call", ["encode few", "encode bulk", "decode", "polar", "prefill", "append few"])
+def test_older_calls_directly_behind_page_calls(libtq, d, call):
+    """Every entry point of the TurboQuant caches behind a fork that exchanges the sequences' pages, with and without
+    a synchronisation between."""
+    B, Hkv, G, T, NB = 8, 2, 4, 960, 18
+    h, pool = tq.tq_init(d, 0), B * Hkv * NB
+    gen = torch.Generator(device="cuda").manual_seed(d)
+    table0 = torch.randperm(pool, generator=gen, device="cuda").to(torch.int32).view(B * Hkv, NB)
+    table, refs = table0.clone(), torch.ones(pool, dtype=torch.int32, device="cuda")
+    polar = call == "polar"
+    caches = [tq.Cache(d, k and not polar, B, Hkv, NB * 64, block_table=table, pool_blocks=pool) for k in (True, False)]
+    pages = tq.Pages(table, refs, Hkv, caches)
+    x = [torch.randn((B, Hkv, T, d), generator=gen, device="cuda").bfloat16() for _ in range(2)]
+    n = 1152 if call == "encode bulk" else 3
+    new = torch.randn((B, Hkv, n, d), generator=gen, device="cuda").bfloat16()
+    Lq = 9
+    q = torch.randn((B, Lq, Hkv * G, d) if call == "prefill" else (B, Hkv * G, d), generator=gen, device="cuda").bfloat16()
+    ws = torch.zeros(max(tq.tq_attend_workspace_bytes(h, B, Hkv * G, Hkv, NB * 64),
+                         tq.tq_prefill_workspace_bytes(h, B, Lq, Hkv * G)), dtype=torch.uint8, device="cuda")
+    swap = i32(np.arange(B) ^ 1)
+    slow = torch.randn((4096, 4096), device="cuda")
+
+    def run(apart):
+        table.copy_(table0)
+        for c, v in zip(caches, x):
+            c.buf.zero_()
+            (tq.tq_encode_k if c.is_k else tq.tq_encode_v)(h, v, c, 0)
+        out = torch.zeros(q.shape, device="cuda")
+        torch.cuda.synchronize()
+        slow @ slow
+        tq.tq_pages_fork(h, pages, swap)
+        if apart:
+            torch.cuda.synchronize()
+        if call.startswith("encode"):
+            for c in caches:
+                (tq.tq_encode_k if c.is_k else tq.tq_encode_v)(h, new, c, 0 if n > 3 else T)
+        elif call == "decode":
+            tq.tq_attend_decode(h, q, *caches, out, ws, T=T, scale=0.09)
+        elif polar:
+            tq.tq_attend_decode_polar(h, q, *caches, out, ws, T=T, scale=0.09)
+        elif call == "prefill":
+            tq.tq_attend_prefill(h, q, *caches, T - Lq, out, ws, scale=0.09)
+        else:
+            tq.tq_append_attend(h, new, new, *caches, T, q, out, ws, scale=0.09)
+        assert tq.tq_device_status(h) == tq.TQ_OK
+        return [out, *(c.buf.clone() for c in caches)]
+
+    want = run(True)
+    for _ in range(3):
+        for a, b in zip(run(False), want):
+            assert torch.equal(a, b)
+    tq.tq_destroy(h)
