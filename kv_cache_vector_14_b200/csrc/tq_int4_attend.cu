@@ -42,9 +42,10 @@
 // Data movement: each warp owns a ring of chunks (codes and pairs of K and V,
 // four bulk copies with an mbarrier); waits are bounded as in the other kernels.
 //
-// Measured: 4 sequences of 102400 tokens, 16/8 heads, d 128, bf16 (floor 72 us): 108 us, 67 %
-// of the copy rate; the copies alone take 82 and the arithmetic alone 85 us.  64 ragged
-// sequences up to 8198 tokens, 32/8 heads, fp16 (floor 55): 119 to 123 us.
+// Measured: 4 sequences of 102400 tokens, 16/8 heads, d 128, bf16 (floor 72 us): 107 to 112 us,
+// 64 to 67 % of the copy rate; the copies alone take 82 and the arithmetic alone 85 us.  fp16 110,
+// fp32 128 us; half as many tokens at d 256: bf16 126, fp32 139.  64 ragged sequences up to 8198
+// tokens, 32/8 heads, fp16 (floor 55): 118 to 123 us.
 #include <type_traits>
 
 #include "tq_frag.cuh"

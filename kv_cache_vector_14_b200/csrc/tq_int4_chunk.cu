@@ -30,11 +30,14 @@
 // to end, shared out evenly over one CTA per SM on the device, cut units merged
 // by the combine kernel, as in tq_int4_attend.cu.
 //
-// Measured: 512 queries after 40448 tokens, 32/8 heads, d 128, bf16: 350 to 380 us (about
-// 0.9 PFLOP/s, 55 % of cuBLAS); a 256 x 64 tile takes about 2000 clocks, of which the tensor
-// pipe and the exponentials fill half each; the softmax warps' chain of waits, loads and
-// stores bounds it.  5 queries of 16 sequences at 4000 tokens: 50 us (20 of 128 rows used; a
-// tile's softmax again).
+// Measured: 512 queries after 40448 tokens, 32/8 heads, d 128, bf16: 342 to 388 us with encode and
+// read-back (0.88 to 1.0 PFLOP/s, 54 to 61 % of cuBLAS); a 256 x 64 tile takes about 2000 clocks, of
+// which the tensor pipe and the exponentials fill half each.  What holds it are the softmax warps:
+// their chain of waits, loads and stores, at 128 registers a thread (14 warps of equal share) of which
+// this kernel spills 356 bytes; how much the spills take of it has not been separated.  The same
+// 512 queries: d 128 fp16 1280, fp32 2520 us (three products of limbs); d 64 bf16 285, fp16 797, fp32
+// 1093.  5 queries of 16 sequences at 4000 tokens, bf16: 50 us (20 of 128 rows used; a tile's softmax
+// again).
 //
 // NaN: a value group with a non-finite pair is expanded as zeros, and the first
 // such token of the segment is kept per group; rows that see it get NaN in that

@@ -8,13 +8,15 @@
 // the group's minimum and maximum are shuffled over group/16 lanes.
 //
 // Both kernels read and write each byte once; HBM bounds them once there are few
-// enough instructions per value (about 9 fit into its time).  So (x - z) r with its
+// enough instructions per value (about 9 fit into its time; the encode below has 15.8, by the
+// count of warp instructions).  So (x - z) r with its
 // clamp to [0, 32] is one saturating multiply by r / 32, rounding to an integer one
 // addition of 1.5 2^18 (where an fp32 ulp is 1/32), the clamp to 15 one packed
 // minimum per two values, and 16-bit inputs take their minimum and maximum two
 // values at a time.  Measured on 262144 vectors of 128 bf16 values (floor 13 us):
-// encode 54 us with 8 values per thread and separate steps, 23 us this way (issue slots
-// 72 % used, ALU 62 %), expand 23 us.
+// encode 54 us with 8 values per thread and separate steps, 21 to 23 us this way (issue slots
+// 72 % used, ALU 62 %), expand 22 to 23 us.  fp32 (floor 23): encode 27, expand 59 us, whose stores
+// of 16 bytes a lane fill half a sector each.
 #include "tq_int4.h"
 
 namespace tqi {
